@@ -463,6 +463,106 @@ caat_status caat_rank_fold(int t, int64_t rows, int64_t cols, caat_dtype dt, con
                            int64_t ld_in, int64_t rank_stride, void *out, int64_t ld_out,
                            caat_stream_t stream);
 
+/*
+ * Serving: what a token step needs between the column-parallel QKV product and the
+ * row-parallel out-projection, and after the last layer.
+ *
+ * The cache of one layer holds pages of `page` tokens (16, 32, 64 or 128).  k and v
+ * are e4m3 codes [pages, kv_heads, page, dim], the last three dimensions dense and
+ * pages page_stride elements apart; k_scale and v_scale are fp32 [pages, kv_heads],
+ * rows scale_stride apart.  A cached value is code * scale; scales are positive
+ * powers of two.  dim is a multiple of 16 up to 128; codes are 16-byte aligned.
+ */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages, page_stride, scale_stride;
+    int32_t kv_heads, page, dim;
+} caat_paged_kv;
+
+/*
+ * The sequences of a step.  The new tokens of all sequences lie one after the other:
+ * rows q_start[b] .. q_start[b + 1] - 1 of the packed tensors belong to sequence b
+ * and take the last places of its kv_len[b] cached tokens (kv_len counts them, in
+ * both calls below).  Token position p of sequence b lies in page page_table[b][p /
+ * page].  A sequence may bring more new tokens than kv_len says (a padded slot of a
+ * captured batch, kv_len 0): its first rows then have no position.  page_table,
+ * q_start (int32[batch + 1]) and kv_len (int32[batch]) are device memory; tokens is
+ * the rows of the packed tensors, q_max the most new tokens of any sequence (it
+ * shapes the launch).  Two sequences may share pages that neither appends to.
+ *
+ * The device-side numbers are checked on the device: a q_start that does not ascend
+ * within [0, tokens], more than q_max new tokens, a kv_len beyond the page table, a
+ * page number outside the cache or a position beyond the angle tables makes no
+ * access out of bounds; it is recorded (caat_get_device_status then returns
+ * CAAT_ERR_INVALID_ARG) and that sequence's results are undefined.
+ */
+typedef struct {
+    const int32_t *page_table, *q_start, *kv_len;
+    int64_t table_stride, tokens;
+    int32_t batch, table_width, q_max;
+} caat_paged_batch;
+
+/*
+ * caat_rope_append -- rotary positions on the new queries and keys; keys and values
+ * quantised into the cache.
+ *
+ * q: [tokens, kv_heads, heads / kv_heads, dim] with strides q_st (token), q_sk (cached
+ * head), q_sg (head of its group); k, v: [tokens, kv_heads, dim] (strides k_st, k_sh
+ * and v_st, v_sh); q_out: [tokens, heads, dim] (qo_st, qo_sh), which may be q itself
+ * with q's strides.  All of type dt, the last dimension dense, strides multiples of 16
+ * bytes.  cos, sin: fp32 [positions, rot / 2], dense: the angles of each position (so
+ * any scaling for long contexts is in the tables).  The first rot values of a head
+ * (a multiple of 16; 0: none, the tables may be null) are turned, in pairs (2i, 2i+1)
+ * if interleaved, else (i, i + rot / 2); each product and sum is one fp32 rounding.
+ * A row without a position gets a q_out of zeros and is not cached.
+ *
+ * Scale of a page and head: the least power of two s with |x| / s <= 448 for every
+ * finite new value x there (at least 2^-100); where the page already holds tokens of
+ * the sequence, not less than its old scale, and the codes of those tokens are
+ * brought to the new one.  Codes round to nearest even; infinities become 448 s; NaN
+ * stays NaN.  Errors: INVALID_ARG (sizes, strides, alignment, null pointers, outputs
+ * that overlap inputs).
+ */
+caat_status caat_rope_append(const caat_paged_kv *kv, const caat_paged_batch *batch, int heads, caat_dtype dt,
+                             const void *q, int64_t q_st, int64_t q_sk, int64_t q_sg,
+                             const void *k, int64_t k_st, int64_t k_sh, const void *v, int64_t v_st, int64_t v_sh,
+                             const float *cos, const float *sin, int64_t positions, int rot, int interleaved,
+                             void *q_out, int64_t qo_st, int64_t qo_sh, caat_stream_t stream);
+
+/*
+ * caat_paged_attention -- softmax attention of the new tokens over the cache.
+ *
+ * q: as for caat_rope_append (rotated); out: [tokens, heads, dim] of type dt (strides
+ * o_st, o_sh).  The query at position p sees the cached keys j <= p; with window > 0
+ * only those with j > p - window or j < sinks.  out = softmax(scale q.k) v; a query
+ * that sees nothing gives zeros.  A NaN in the cache reaches the queries that see it
+ * and no others.  Scores, sums and outputs are held in fp32; bf16 queries and the
+ * weights enter the tensor cores as f16 (fp32: as two f16).  Errors: INVALID_ARG.
+ */
+caat_status caat_paged_attention(const caat_paged_kv *kv, const caat_paged_batch *batch, int heads, caat_dtype dt,
+                                 const void *q, int64_t q_st, int64_t q_sk, int64_t q_sg, float scale,
+                                 int window, int sinks, void *out, int64_t o_st, int64_t o_sh,
+                                 caat_stream_t stream);
+
+/*
+ * caat_sample_tokens -- the next token of each row of logits [batch, vocab] (row
+ * stride ld, type dt) from the uniform numbers u[batch] in [0, 1).
+ *
+ * With w_i = exp((z_i - max z) / temperature) and the tokens ordered by logit (equal
+ * logits by index): the first top_k (<= 0: all); of those the shortest prefix whose
+ * weights reach top_p of their sum (>= 1: all); of those w_i >= min_p (0: all); the
+ * first of the order always stays.  The token is the lowest index i with sum of the
+ * kept w_j, j <= i, above u times their sum.  temperature <= 0: the largest logit, the
+ * lowest index of equals.  temperature, top_k (int32), top_p, min_p: device arrays of
+ * batch numbers.  token: int32[batch]; logprob: fp32[batch], log softmax(z) of the
+ * token, before temperature and filters.  NaN counts as -inf; a row of nothing else
+ * gives token -1 and logprob -inf.  vocab < 2^31.  Errors: INVALID_ARG.
+ */
+caat_status caat_sample_tokens(int64_t batch, int64_t vocab, caat_dtype dt, const void *logits, int64_t ld,
+                               const float *u, const float *temperature, const int32_t *top_k, const float *top_p,
+                               const float *min_p, int32_t *token, float *logprob, caat_stream_t stream);
+
 /* Human-readable name of a status code (static string, never null). */
 const char *caat_status_string(caat_status st);
 
@@ -471,7 +571,9 @@ const char *caat_status_string(caat_status st);
  * library's device-side error word of the current device.  Every wait inside the
  * tensor-core kernels is bounded; a wait that gives up records CAAT_ERR_TIMEOUT
  * there and the kernel exits (its outputs are then undefined) instead of hanging.
- * Returns CAAT_ERR_CUDA when the synchronization itself fails.
+ * The serving kernels record CAAT_ERR_INVALID_ARG there for lengths, pages and
+ * positions that do not fit their buffers.  Returns CAAT_ERR_CUDA when the
+ * synchronization itself fails.
  */
 caat_status caat_get_device_status(caat_stream_t stream);
 

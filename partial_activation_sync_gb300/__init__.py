@@ -25,7 +25,7 @@ __all__ = [
     "colpar_linear_bwd", "colpar_linear_bwd_workspace", "device_status", "last_kernel", "launch_count",
     "debug_set_wait", "CAAT_INJECT_NONE", "CAAT_INJECT_SKIP_LOADS", "pcr_pack", "pcr_unpack", "rank_fold",
     "CaatError", "CAAT_S_CONTIGUOUS", "CAAT_S_RANDOM", "CAAT_BWD_REDUCE_DOUT",
-    "CAAT_BWD_NO_REDUCE",
+    "CAAT_BWD_NO_REDUCE", "PagedKVCache", "PagedBatch", "rope_append", "paged_attention", "sample_tokens",
 ]
 
 
@@ -533,3 +533,8 @@ def rowpar_linear_bwd_noalloc(X, W, dOut, t: int, sel, mode: int = CAAT_BWD_REDU
            ctypes.c_void_p(dW.data_ptr()), dw_rs, dw_cs, sp, ns, int(mode), _stream_ptr(stream))
     _check(st, "caat_rowpar_linear_bwd_noalloc")
     return dX, dW
+
+
+# ------------------------------------------------------------------ serving
+
+from .serving import PagedBatch, PagedKVCache, paged_attention, rope_append, sample_tokens  # noqa: E402

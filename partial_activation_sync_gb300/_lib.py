@@ -33,7 +33,24 @@ EXPORTS = (
     "caat_pcr_pack",
     "caat_pcr_unpack",
     "caat_rank_fold",
+    "caat_rope_append",
+    "caat_paged_attention",
+    "caat_sample_tokens",
 )
+
+
+class PagedKV(ctypes.Structure):
+    """caat_paged_kv"""
+    _fields_ = [("k", _c_p), ("v", _c_p), ("k_scale", _c_p), ("v_scale", _c_p), ("pages", _c_i64),
+                ("page_stride", _c_i64), ("scale_stride", _c_i64), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("dim", ctypes.c_int32)]
+
+
+class PagedBatch(ctypes.Structure):
+    """caat_paged_batch"""
+    _fields_ = [("page_table", _c_p), ("q_start", _c_p), ("kv_len", _c_p), ("table_stride", _c_i64),
+                ("tokens", _c_i64), ("batch", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("q_max", ctypes.c_int32)]
 
 _lib = None
 
@@ -113,6 +130,17 @@ def load(path: str = None) -> ctypes.CDLL:
     L.caat_rank_fold.argtypes = [ctypes.c_int, _c_i64, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_i64, _c_p, _c_i64,
                                  _c_p]
     L.caat_rank_fold.restype = ctypes.c_int
+    L.caat_rope_append.argtypes = [ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), ctypes.c_int, ctypes.c_int,
+                                   _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64,
+                                   _c_p, _c_p, _c_i64, ctypes.c_int, ctypes.c_int, _c_p, _c_i64, _c_i64, _c_p]
+    L.caat_rope_append.restype = ctypes.c_int
+    L.caat_paged_attention.argtypes = [ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), ctypes.c_int,
+                                       ctypes.c_int, _c_p, _c_i64, _c_i64, _c_i64, ctypes.c_float, ctypes.c_int,
+                                       ctypes.c_int, _c_p, _c_i64, _c_i64, _c_p]
+    L.caat_paged_attention.restype = ctypes.c_int
+    L.caat_sample_tokens.argtypes = [_c_i64, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                     _c_p, _c_p, _c_p]
+    L.caat_sample_tokens.restype = ctypes.c_int
     if path is None:
         _lib = L
     return L

@@ -157,4 +157,19 @@ caat_status launch_rowpar_bwd_tc(int t, int64_t N, int64_t K, int64_t h, const v
 caat_status launch_permute_rows(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t h, int64_t K,
                                 const int32_t *sel, int64_t n_sel, bool to_s_first, cudaStream_t s);
 
+// ---- serving (serve.cu checks the arguments; paged.cuh holds the types)
+struct PagedKV;
+struct PagedBatch;
+caat_status launch_rope_append(const PagedKV &kv, const PagedBatch &pb, int heads, caat_dtype dt, const void *q,
+                               int64_t q_st, int64_t q_sk, int64_t q_sg, const void *k, int64_t k_st, int64_t k_sh,
+                               const void *v, int64_t v_st, int64_t v_sh, const float *cos, const float *sin,
+                               int64_t positions, int rot, bool interleaved, void *qo, int64_t qo_st, int64_t qo_sh,
+                               cudaStream_t s);
+caat_status launch_paged_attention(const PagedKV &kv, const PagedBatch &pb, int heads, caat_dtype dt, const void *q,
+                                   int64_t q_st, int64_t q_sk, int64_t q_sg, float scale, int window, int sinks,
+                                   void *o, int64_t o_st, int64_t o_sh, cudaStream_t s);
+caat_status launch_sample_tokens(int64_t B, int64_t V, caat_dtype dt, const void *logits, int64_t ld, const float *u,
+                                 const float *temperature, const int32_t *top_k, const float *top_p,
+                                 const float *min_p, int32_t *token, float *logprob, cudaStream_t s);
+
 }  // namespace caat

@@ -53,6 +53,7 @@ __device__ int g_caat_dev_error;
 
 caat_status read_and_clear_bwd_error();
 caat_status read_and_clear_skinny_error();
+caat_status read_and_clear_serve_error();
 
 caat_status read_and_clear_device_error()
 {
@@ -60,6 +61,8 @@ caat_status read_and_clear_device_error()
     if (sb != CAAT_OK) return sb;
     const caat_status ss = read_and_clear_skinny_error();
     if (ss != CAAT_OK) return ss;
+    const caat_status sv = read_and_clear_serve_error();
+    if (sv != CAAT_OK) return sv;
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_caat_dev_error, sizeof(int)) != cudaSuccess) return CAAT_ERR_CUDA;
     if (v != 0) {

@@ -1,0 +1,82 @@
+// Shared by the kernels that write and read the paged 8-bit key-value cache: what a
+// launch gets of the cache and the batch, the bounds checks of the device-side
+// indices, and the e4m3 conversions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "caat_internal.h"
+
+namespace caat {
+
+struct PagedKV {
+    uint8_t *k, *v;                  // codes [pages][kv_heads][page][dim]
+    float *ks, *vs;                  // scales [pages][kv_heads]
+    int64_t page_stride;             // elements from one page to the next
+    int64_t scale_stride;            // scales from one page to the next
+    int64_t pages;
+    int kv_heads, page, log2_page, dim;
+};
+
+struct PagedBatch {
+    const int32_t *table;            // [batch][width], row stride table_stride
+    const int32_t *q_start, *kv_len;
+    int64_t table_stride, tokens;
+    int batch, width, q_max;
+};
+
+// The new tokens of one sequence: tokens [t0, t0 + n) of the packed rows at cache
+// positions [pos0, pos0 + n).  pos0 < 0 when the cache holds fewer tokens than the
+// call brings; the tokens below position 0 then see nothing and are not stored.
+struct Seq {
+    int64_t t0;
+    int n, pos0, len;
+    bool ok;
+};
+
+// Reads and checks the lengths of sequence b; a sequence whose numbers do not fit
+// the buffers is recorded in *err and reported as not ok.
+__device__ __forceinline__ Seq load_seq(const PagedBatch &pb, int page, int b, int *err)
+{
+    Seq s;
+    const int a = __ldg(pb.q_start + b), e = __ldg(pb.q_start + b + 1);
+    s.len = __ldg(pb.kv_len + b);
+    s.t0 = a;
+    s.n = e - a;
+    s.pos0 = s.len - s.n;
+    s.ok = a >= 0 && e >= a && (int64_t)e <= pb.tokens && s.n <= pb.q_max && s.len >= 0 &&
+           (int64_t)s.len <= (int64_t)pb.width * page;
+    if (!s.ok) {
+        *(volatile int *)err = CAAT_ERR_INVALID_ARG;
+        s.n = 0;
+    }
+    return s;
+}
+
+// a page number of the table, or -1 (recorded in *err) when the cache has no such page
+__device__ __forceinline__ int64_t checked_page(int id, const PagedKV &kv, int *err)
+{
+    if (id >= 0 && (int64_t)id < kv.pages) return id;
+    *(volatile int *)err = CAAT_ERR_INVALID_ARG;
+    return -1;
+}
+
+// two e4m3 codes (low byte first) -> two f16, exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// two floats -> two e4m3 codes, nearest even, magnitudes above 448 to 448, NaN kept
+__device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi)
+{
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+int *serve_error_word();             // device address of these kernels' error word, or null
+caat_status read_and_clear_serve_error();
+
+}  // namespace caat

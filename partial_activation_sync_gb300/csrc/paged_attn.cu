@@ -1,0 +1,555 @@
+// Attention of a few query rows over a paged 8-bit key-value cache.
+//
+// Row i at position p sees the keys j <= p (with a window w: j > p - w or j < sinks):
+//     o = sum_j e^(c q.k_j - m) v_j / sum_j e^(c q.k_j - m),   m = max_j c q.k_j
+// in one pass over the cache: each warp carries the running maximum, sum and o of its
+// share of the keys, and the shares are joined at the end, first over the warps of a
+// block through shared memory, then over the blocks of a cluster through theirs.  A
+// cluster per cached head and sequence needs no workspace, no second launch and no
+// atomics, and the order of every sum is fixed.
+//
+// Bound by the cache's bytes.  The rows of a launch are the query heads that share a
+// cached head, times the new tokens: up to 16 of them go through the cache together,
+// as the narrow side of m16n8k16 products whose wide side is the cache (scores: keys
+// x head dimension; output: head dimension x keys).  mma.sync and not tcgen05: the
+// products take a few percent of the time the bytes take, and their fragments can be
+// filled from 16-byte global loads without shared memory.  Which key and which
+// dimension a fragment element stands for is free as long as both operands agree, so
+// each lane takes 16 consecutive codes of one key, and of four keys' values; the
+// latter become pairs along the keys by byte permutes.
+//
+// Codes become f16, which holds every e4m3 value.  Queries become f16 times a power
+// of two for each row, and weights f16 times 2^8: 11 bits against the 8 of bf16, at
+// the same speed.  fp32 queries are split into two f16 (22 bits), as are the weights,
+// at twice the products.  The scales of a page multiply the scores after the product
+// (keys) and the weights before it (values), in fp32.
+#include "paged.cuh"
+#include "tc_ptx.cuh"
+
+namespace caat {
+namespace {
+
+using tc::cluster_sync;
+using tc::map_to_cta;
+using tc::smem_u32;
+
+constexpr int WARPS = 4;
+constexpr float P_BIAS = 8.f;        // weights are held times 2^8
+
+struct AttnParams {
+    const void *q;
+    int64_t q_st, q_sk, q_sg;
+    void *o;
+    int64_t o_st, o_sh;
+    float scale_log2;                // softmax scale * log2 e
+    int window, sinks;               // window 0: none
+    int heads, group, chunks;        // row chunks of a sequence and cached head
+    int *err;
+    PagedKV kv;
+    PagedBatch pb;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 matrix of 16-bit values over a warp, transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// what pack_f16 rounded away
+__device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&packed));
+    return pack_f16(lo - f.x, hi - f.y);
+}
+
+template <int B>                     // B = 16 or 8 codes of one row, read once
+__device__ __forceinline__ void load_codes(uint32_t (&w)[B / 4], const uint8_t *p, bool live)
+{
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) w[i] = 0;
+    if (!live) return;
+    if constexpr (B == 16) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "l"(p));
+    } else {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    }
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// four bytes: 0xff where the code is NaN (0x7f or 0xff)
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// DP: head dimension rounded up to 64 or 128.  NT: row tiles of 8.  F32: fp32
+// queries and output (both operands of the products in two f16 parts).
+template <int DP, int NT, bool F32>
+struct Geo {
+    static constexpr int NJ = DP / 64;           // 16-code loads of a key for each lane
+    static constexpr int VB = DP / 8;            // value codes of one key for each lane
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int PART = DP + 4;          // floats of one row's share: o, m, l, pad
+};
+
+// The codes of one group of 16 keys, as one lane holds them.
+template <int DP>
+struct Codes {
+    uint32_t k[2][DP / 64][4];                   // keys r and r + 8
+    uint32_t v[4][DP / 32];                      // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    float ks, vs;
+};
+
+template <int DP, int NT, bool F32>
+__global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_attn_few_kernel(AttnParams p, int splits)
+{
+    using G = Geo<DP, NT, F32>;
+    extern __shared__ float sm[];                // [WARPS + 1][ROWS][PART]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane >> 2, c = lane & 3;
+    const int split = (int)(blockIdx.x % splits);
+    int64_t unit = blockIdx.x / splits;
+    const int chunk = (int)(unit % p.chunks);
+    unit /= p.chunks;
+    const int h = (int)(unit % p.kv.kv_heads), b = (int)(unit / p.kv.kv_heads);
+    const int P = p.kv.page, D = p.kv.dim;
+
+    const Seq sq = load_seq(p.pb, P, b, p.err);
+    const int rows_all = sq.n * p.group;
+    const int row0 = chunk * G::ROWS;
+    if (row0 >= rows_all) return;                // the whole cluster: same sequence and chunk
+    const int rows = min(G::ROWS, rows_all - row0);
+    const int p_lo = sq.pos0 + row0 / p.group, p_hi = sq.pos0 + (row0 + rows - 1) / p.group;
+
+    // groups of 16 keys that some row sees: those of the first tokens, then the window's
+    const int win_lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
+    const int g_lo = win_lo >> 4;
+    const int n_sink = min((p.sinks + 15) >> 4, g_lo);
+    const int n_grp = p_hi < 0 ? 0 : n_sink + ((p_hi >> 4) + 1 - g_lo);
+
+    // queries of this lane: rows 8t + r, codes' dimensions (c + 4j) * 16 .. + 15
+    uint32_t qh[NT][G::NJ][8], ql[NT][G::NJ][F32 ? 8 : 1];
+    float qf[NT][2];                             // scale of rows 8t + 2c, 8t + 2c + 1
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int row = row0 + 8 * t + r;
+        const bool live = 8 * t + r < rows;
+        float x[G::NJ][16];
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j) {
+            const int d = (c + 4 * j) * 16;
+            const bool in = live && d < D;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[j][i] = 0.f;
+            if (in) {
+                const int hg = row % p.group;
+                const int64_t at = (sq.t0 + row / p.group) * p.q_st + h * p.q_sk + hg * p.q_sg + d;
+                if constexpr (F32) {
+                    const float4 *s = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.q) + at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 f = __ldg(s + i);
+                        x[j][4 * i] = f.x, x[j][4 * i + 1] = f.y, x[j][4 * i + 2] = f.z, x[j][4 * i + 3] = f.w;
+                    }
+                } else {
+                    const uint4 *s = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p.q) + at);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 f = __ldg(s + i);
+                        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[j][8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+                            x[j][8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float a = fabsf(x[j][i]);
+                m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);
+            }
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // a power of two that brings the largest magnitude to [2^14, 2^15)
+        const int e = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 127, -100) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + min(14 - e, 120)) << 23);
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = x[j][2 * i] * up, z = x[j][2 * i + 1] * up;
+                qh[t][j][i] = pack_f16(a, z);
+                if constexpr (F32) ql[t][j][i] = pack_f16_rest(a, z, qh[t][j][i]);
+            }
+        const float down = p.scale_log2 / up;
+        qf[t][0] = __shfl_sync(0xffffffffu, down, (2 * c) * 4);
+        qf[t][1] = __shfl_sync(0xffffffffu, down, (2 * c + 1) * 4);
+    }
+
+    float o[NT][G::VB / 2][4], mx[NT][2], sum[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int i = 0; i < G::VB / 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+        mx[t][0] = mx[t][1] = -INFINITY;
+        sum[t][0] = sum[t][1] = 0.f;
+    }
+    float ref = 0.f;                             // o counts in units of this value scale
+
+    const int32_t *table = p.pb.table + (int64_t)b * p.pb.table_stride;
+    const uint8_t *kbase = p.kv.k + (int64_t)h * P * D, *vbase = p.kv.v + (int64_t)h * P * D;
+    auto group_of = [&](int i) { return i < n_sink ? i : g_lo + i - n_sink; };
+    auto page_of = [&](int i) { return i < n_grp ? __ldg(table + ((group_of(i) << 4) >> p.kv.log2_page)) : 0; };
+    auto load = [&](Codes<DP> &x, int i, int id) {
+        int64_t pg = 0;
+        if (i < n_grp) pg = checked_page(id, p.kv, p.err);
+        const bool live = i < n_grp && pg >= 0;
+        if (!live) pg = 0;
+        const int at = (group_of(i) << 4) & (P - 1);
+        const uint8_t *kp = kbase + pg * p.kv.page_stride + (int64_t)at * D;
+        const uint8_t *vp = vbase + pg * p.kv.page_stride + (int64_t)at * D;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < G::NJ; ++j)
+                load_codes<16>(x.k[u][j], kp + (r + 8 * u) * D + (c + 4 * j) * 16, live && (c + 4 * j) * 16 < D);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            load_codes<G::VB>(x.v[u], vp + (2 * c + (u & 1) + 8 * (u >> 1)) * D + r * G::VB, live && r * G::VB < D);
+        x.ks = live ? __ldg(p.kv.ks + pg * p.kv.scale_stride + h) : 1.f;
+        x.vs = live ? __ldg(p.kv.vs + pg * p.kv.scale_stride + h) : 1.f;
+    };
+
+    auto consume = [&](Codes<DP> &x, int i) {
+        const int k0 = group_of(i) << 4;
+        float s[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < G::NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a0 = e4m3x2_f16x2(x.k[0][j][e] & 0xffffu), a2 = e4m3x2_f16x2(x.k[0][j][e] >> 16);
+                const uint32_t a1 = e4m3x2_f16x2(x.k[1][j][e] & 0xffffu), a3 = e4m3x2_f16x2(x.k[1][j][e] >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma16816(s[t], a0, a1, a2, a3, qh[t][j][2 * e], qh[t][j][2 * e + 1]);
+                    if constexpr (F32) mma16816(s[t], a0, a1, a2, a3, ql[t][j][2 * e], ql[t][j][2 * e + 1]);
+                }
+            }
+        // every row sees every key of the group?
+        const bool all = k0 + 15 <= p_lo && (p.window == 0 || k0 > p_hi - p.window || k0 + 15 < p.sinks);
+        float ratio = 1.f, shrink = 1.f;
+        if (x.vs != ref) {                       // same for the warp
+            if (x.vs > ref * 0x1p-24f) {
+                shrink = ref / x.vs;
+                ref = x.vs;
+            } else {
+                ratio = x.vs / ref;
+            }
+        }
+        uint32_t ph[NT][2], pl[NT][2], vis[NT][2];
+        float alpha[NT][2];
+        bool same = shrink == 1.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uint32_t seen[4] = {1u, 1u, 1u, 1u};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] *= x.ks * qf[t][e & 1];
+            if (!all) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = k0 + r + 8 * (e >> 1);
+                    const int pos = sq.pos0 + (row0 + 8 * t + 2 * c + (e & 1)) / p.group;
+                    const bool see = key <= pos && (p.window == 0 || key > pos - p.window || key < p.sinks);
+                    seen[e] = see;
+                    if (!see) s[t][e] = -INFINITY;
+                }
+            }
+            vis[t][0] = seen[0] * 0x3c00u | seen[1] * 0x3c000000u;       // f16 ones
+            vis[t][1] = seen[2] * 0x3c00u | seen[3] * 0x3c000000u;
+            float m0 = fmaxf(s[t][0], s[t][2]), m1 = fmaxf(s[t][1], s[t][3]);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) {
+                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, w));
+                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, w));
+            }
+            m0 = fmaxf(m0, mx[t][0]);
+            m1 = fmaxf(m1, mx[t][1]);
+            // a row that has seen nothing yet subtracts 0 from scores that are all -inf
+            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+            alpha[t][0] = exp2_approx(mx[t][0] - u0);
+            alpha[t][1] = exp2_approx(mx[t][1] - u1);
+            mx[t][0] = m0;
+            mx[t][1] = m1;
+            const float e0 = exp2_approx(s[t][0] - u0 + P_BIAS), e1 = exp2_approx(s[t][1] - u1 + P_BIAS);
+            const float e2 = exp2_approx(s[t][2] - u0 + P_BIAS), e3 = exp2_approx(s[t][3] - u1 + P_BIAS);
+            sum[t][0] = sum[t][0] * alpha[t][0] + (e0 + e2);
+            sum[t][1] = sum[t][1] * alpha[t][1] + (e1 + e3);
+            const float w0 = e0 * ratio, w1 = e1 * ratio, w2 = e2 * ratio, w3 = e3 * ratio;
+            ph[t][0] = pack_f16(w0, w1);
+            ph[t][1] = pack_f16(w2, w3);
+            if constexpr (F32) {
+                pl[t][0] = transpose8x8(pack_f16_rest(w0, w1, ph[t][0]));
+                pl[t][1] = transpose8x8(pack_f16_rest(w2, w3, ph[t][1]));
+            }
+            ph[t][0] = transpose8x8(ph[t][0]);
+            ph[t][1] = transpose8x8(ph[t][1]);
+            same = same && alpha[t][0] == 1.f && alpha[t][1] == 1.f;
+        }
+        if (!__all_sync(0xffffffffu, same)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float f0 = alpha[t][0] * shrink, f1 = alpha[t][1] * shrink;
+#pragma unroll
+                for (int d = 0; d < G::VB / 2; ++d) {
+                    o[t][d][0] *= f0, o[t][d][2] *= f0;
+                    o[t][d][1] *= f1, o[t][d][3] *= f1;
+                }
+            }
+        }
+        if (!all) {
+            // A NaN value must reach the rows that see its key and no other: take the
+            // NaN codes out, and where there are any, count for each row and dimension
+            // the ones it sees (the same product with ones in place of the weights).
+            uint32_t any = 0, bad[4][DP / 32];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int w = 0; w < DP / 32; ++w) {
+                    bad[u][w] = nan_bytes(x.v[u][w]);
+                    any |= bad[u][w];
+                    x.v[u][w] &= ~bad[u][w];
+                    bad[u][w] &= 0x38383838u;    // e4m3 one
+                }
+            if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t b0 = transpose8x8(vis[t][0]), b1 = transpose8x8(vis[t][1]);
+#pragma unroll
+                    for (int d = 0; d < G::VB / 2; ++d) {
+                        float n[4] = {};
+                        const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2, sh = 8 * (d & 3);
+                        auto pair = [&](int u, int w) {
+                            return e4m3x2_f16x2(((bad[u][w] >> sh) & 0xffu) | (((bad[u + 1][w] >> sh) & 0xffu) << 8));
+                        };
+                        mma16816(n, pair(0, w0), pair(0, w1), pair(2, w0), pair(2, w1), b0, b1);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n[e] > 0.f) o[t][d][e] = __int_as_float(0x7fffffff);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < G::VB / 2; d += 2) {
+            // dimensions r * VB + d, d + 1 (rows r) and + VB / 2 (rows r + 8)
+            const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2;
+            const uint32_t pick = (d & 2) ? 0x7362u : 0x5140u;
+            const uint32_t x0 = __byte_perm(x.v[0][w0], x.v[1][w0], pick), x1 = __byte_perm(x.v[0][w1], x.v[1][w1], pick);
+            const uint32_t x2 = __byte_perm(x.v[2][w0], x.v[3][w0], pick), x3 = __byte_perm(x.v[2][w1], x.v[3][w1], pick);
+            const uint32_t a0 = e4m3x2_f16x2(x0 & 0xffffu), a1 = e4m3x2_f16x2(x1 & 0xffffu);
+            const uint32_t a2 = e4m3x2_f16x2(x2 & 0xffffu), a3 = e4m3x2_f16x2(x3 & 0xffffu);
+            const uint32_t e0 = e4m3x2_f16x2(x0 >> 16), e1 = e4m3x2_f16x2(x1 >> 16);
+            const uint32_t e2 = e4m3x2_f16x2(x2 >> 16), e3 = e4m3x2_f16x2(x3 >> 16);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mma16816(o[t][d], a0, a1, a2, a3, ph[t][0], ph[t][1]);
+                mma16816(o[t][d + 1], e0, e1, e2, e3, ph[t][0], ph[t][1]);
+                if constexpr (F32) {
+                    mma16816(o[t][d], a0, a1, a2, a3, pl[t][0], pl[t][1]);
+                    mma16816(o[t][d + 1], e0, e1, e2, e3, pl[t][0], pl[t][1]);
+                }
+            }
+        }
+    };
+
+    // groups are dealt round-robin to the warps of the cluster; the next group's codes
+    // are on their way while one is worked on, and the page number after that
+    {
+        const int step = splits * WARPS;
+        int i = split * WARPS + warp;
+        Codes<DP> x, y;
+        load(x, i, page_of(i));
+        int id = page_of(i + step);
+        while (i < n_grp) {
+            load(y, i + step, id);
+            id = page_of(i + 2 * step);
+            consume(x, i);
+            i += step;
+            if (i >= n_grp) break;
+            load(x, i + step, id);
+            id = page_of(i + 2 * step);
+            consume(y, i);
+            i += step;
+        }
+    }
+
+    // shares of this warp to shared memory: o in units of 2^-P_BIAS, as is the sum
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) sum[t][e] += __shfl_xor_sync(0xffffffffu, sum[t][e], w);
+            float *part = sm + (warp * G::ROWS + 8 * t + 2 * c + e) * G::PART;
+#pragma unroll
+            for (int d = 0; d < G::VB / 2; d += 4) {
+                *reinterpret_cast<float4 *>(part + r * G::VB + d) =
+                    make_float4(o[t][d][e] * ref, o[t][d + 1][e] * ref, o[t][d + 2][e] * ref, o[t][d + 3][e] * ref);
+                *reinterpret_cast<float4 *>(part + r * G::VB + G::VB / 2 + d) =
+                    make_float4(o[t][d][2 + e] * ref, o[t][d + 1][2 + e] * ref, o[t][d + 2][2 + e] * ref,
+                                o[t][d + 3][2 + e] * ref);
+            }
+            if (r == 0) {
+                part[DP] = mx[t][e];
+                part[DP + 1] = sum[t][e];
+            }
+        }
+    __syncthreads();
+    // join the warps: row by row, one thread for a dimension
+    float *mine = sm + WARPS * G::ROWS * G::PART;
+    for (int i = threadIdx.x; i < rows * DP; i += WARPS * 32) {
+        const int row = i / DP, d = i % DP;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm[(w * G::ROWS + row) * G::PART + DP]);
+        float a = 0.f, l = 0.f;
+        const float u = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float *part = sm + (w * G::ROWS + row) * G::PART;
+            const float f = exp2_approx(part[DP] - u);
+            a += part[d] * f;
+            l += part[DP + 1] * f;
+        }
+        mine[row * G::PART + d] = a;
+        if (d == 0) {
+            mine[row * G::PART + DP] = m;
+            mine[row * G::PART + DP + 1] = l;
+        }
+    }
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    // join the blocks: each takes its share of the rows' dimensions
+    const uint32_t base = smem_u32(mine);
+    for (int i = split * WARPS * 32 + (int)threadIdx.x; i < rows * DP; i += splits * WARPS * 32) {
+        const int row = i / DP, d = i % DP;
+        if (d >= D) continue;
+        const uint32_t at = base + (uint32_t)(row * G::PART) * 4u;
+        float a = 0.f, l = 0.f;
+        if (splits == 1) {
+            a = mine[row * G::PART + d];
+            l = mine[row * G::PART + DP + 1];
+        } else {
+            float m = -INFINITY;
+            for (int k = 0; k < splits; ++k) m = fmaxf(m, ld_cluster(map_to_cta(at + DP * 4u, (uint32_t)k)));
+            const float u = m == -INFINITY ? 0.f : m;
+            for (int k = 0; k < splits; ++k) {
+                const float f = exp2_approx(ld_cluster(map_to_cta(at + DP * 4u, (uint32_t)k)) - u);
+                a += ld_cluster(map_to_cta(at + d * 4u, (uint32_t)k)) * f;
+                l += ld_cluster(map_to_cta(at + DP * 4u + 4u, (uint32_t)k)) * f;
+            }
+        }
+        const float v = l == 0.f ? 0.f : a / l;      // NaN stays NaN; a row that sees nothing is 0
+        const int64_t t = sq.t0 + (row0 + row) / p.group;
+        const int head = h * p.group + (row0 + row) % p.group;
+        const int64_t out = t * p.o_st + head * p.o_sh + d;
+        if constexpr (F32) reinterpret_cast<float *>(p.o)[out] = v;
+        else reinterpret_cast<__nv_bfloat16 *>(p.o)[out] = __float2bfloat16_rn(v);
+    }
+    if (splits > 1) cluster_sync();              // no block leaves while another reads its shares
+}
+
+template <int DP, int NT, bool F32>
+caat_status launch_few(AttnParams &p, cudaStream_t s)
+{
+    using G = Geo<DP, NT, F32>;
+    const int64_t rows = (int64_t)p.pb.q_max * p.group;
+    const int64_t chunks = (rows + G::ROWS - 1) / G::ROWS;
+    const int64_t units = (int64_t)p.pb.batch * p.kv.kv_heads * chunks;
+    if (chunks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+    p.chunks = (int)chunks;
+    // blocks for each unit: enough to fill the SMs twice, while each warp still gets two
+    // groups of 16 keys of the longest sequence the page table can hold
+    int64_t keys = (int64_t)p.pb.width * p.kv.page;
+    if (p.window > 0 && keys > (int64_t)p.window + p.sinks + p.pb.q_max) keys = (int64_t)p.window + p.sinks + p.pb.q_max;
+    int splits = 1;
+    while (splits < 16 && units * splits < 6 * (int64_t)num_sms() && keys > (int64_t)splits * WARPS * 32) splits *= 2;
+    if (units * splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+    auto kern = paged_attn_few_kernel<DP, NT, F32>;
+    const int smem = (WARPS + 1) * G::ROWS * G::PART * 4;
+    if (prepare_kernel_smem((const void *)kern, smem) != CAAT_OK) return CAAT_ERR_CUDA;
+    if (splits > 8 && cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                          cudaSuccess)
+        return CAAT_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(units * splits));
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, p, splits) != cudaSuccess) return CAAT_ERR_CUDA;
+    note_launch("paged_attn_few");
+    return CAAT_OK;
+}
+
+}  // namespace
+
+caat_status launch_paged_attention(const PagedKV &kv, const PagedBatch &pb, int heads, caat_dtype dt, const void *q,
+                                   int64_t q_st, int64_t q_sk, int64_t q_sg, float scale, int window, int sinks,
+                                   void *o, int64_t o_st, int64_t o_sh, cudaStream_t s)
+{
+    AttnParams p{q, q_st, q_sk, q_sg, o, o_st, o_sh, scale * 1.4426950408889634f, window, sinks, heads,
+                 heads / kv.kv_heads, 1, serve_error_word(), kv, pb};
+    if (p.err == nullptr) return CAAT_ERR_CUDA;
+    const bool wide = (int64_t)pb.q_max * p.group > 8;
+    if (dt == CAAT_F32) {
+        if (kv.dim <= 64) return launch_few<64, 1, true>(p, s);
+        return launch_few<128, 1, true>(p, s);
+    }
+    if (kv.dim <= 64) return wide ? launch_few<64, 2, false>(p, s) : launch_few<64, 1, false>(p, s);
+    return wide ? launch_few<128, 2, false>(p, s) : launch_few<128, 1, false>(p, s);
+}
+
+}  // namespace caat

@@ -1,0 +1,301 @@
+// Rotary positions on new queries and keys, and the new keys and values into a
+// paged 8-bit cache, in one launch.
+//
+// Rotation of a pair (a, b) of a head at position p, angle table entry i:
+//     a' = a cos[p, i] - b sin[p, i],   b' = b cos[p, i] + a sin[p, i]
+// in fp32, each product and sum rounded by itself (no contraction), so the codes do
+// not depend on how a compiler fuses them.  The pairs are (2i, 2i + 1) or
+// (i, i + rot / 2); values from rot on pass through.
+//
+// Cache: value = code * scale, one scale for a page and head, a power of two: e4m3
+// is a floating type, so a finer scale buys no relative precision, and with powers
+// of two the division by the scale and the change of scale are exact.  A page that
+// already holds tokens of the sequence keeps its scale unless the new rows need a
+// larger one; its codes are then brought to the new scale (an exact shift but for
+// codes that reach the subnormals, which round to nearest even).
+//
+// Bound by memory: the queries, keys and values once, the codes once.  One thread
+// holds 16 values of one token row (a pair slot), so both halves of every rotated
+// pair and the 16-byte store of the codes are its own.
+#include "paged.cuh"
+
+namespace caat {
+namespace {
+
+struct AppendParams {
+    const void *q, *k, *v;
+    int64_t q_st, q_sk, q_sg;        // q strides: token, cached head, head within its group
+    int64_t k_st, k_sh, v_st, v_sh;
+    void *qo;
+    int64_t qo_st, qo_sh;
+    const float *cos, *sin;          // [positions][rot / 2]
+    int64_t positions;
+    int heads, group, rot;
+    int *err;
+    PagedKV kv;
+    PagedBatch pb;
+};
+
+__device__ __forceinline__ void load8(const float *p, float (&x)[16], int at)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[at] = a.x, x[at + 1] = a.y, x[at + 2] = a.z, x[at + 3] = a.w;
+    x[at + 4] = b.x, x[at + 5] = b.y, x[at + 6] = b.z, x[at + 7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[16], int at)
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[at + 2 * i] = __uint_as_float(w[i] << 16);
+        x[at + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void store8(float *p, const float (&x)[16], int at)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(x[at], x[at + 1], x[at + 2], x[at + 3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[at + 4], x[at + 5], x[at + 6], x[at + 7]);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[16], int at)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[at + 2 * i], x[at + 2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Where the 16 values of pair slot s lie in a head: two runs of 8.  For the half
+// layout the runs of a rotated slot are the two sides of its pairs; otherwise they
+// are neighbours.
+template <bool INTER>
+__device__ __forceinline__ void slot_runs(int s, int rot, int &d0, int &d1)
+{
+    if (!INTER && 16 * s < rot) d0 = 8 * s, d1 = 8 * s + rot / 2;
+    else d0 = 16 * s, d1 = 16 * s + 8;
+}
+
+// In both layouts the angles of a rotated slot are entries 8s .. 8s + 7.
+template <bool INTER>
+__device__ __forceinline__ void rotate16(float (&x)[16], const float (&c)[8], const float (&s)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float &a = x[INTER ? 2 * i : i], &b = x[INTER ? 2 * i + 1 : i + 8];
+        const float na = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+        const float nb = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+        a = na;
+        b = nb;
+    }
+}
+
+// the largest finite magnitude
+__device__ __forceinline__ float amax16(const float (&x)[16])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float a = fabsf(x[i]);
+        m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);     // false for NaN too
+    }
+    return m;
+}
+
+// least power of two s with m / s <= 448 = 1.75 * 2^8, not below 2^-100
+__device__ __forceinline__ float pow2_scale(float m)
+{
+    const uint32_t u = __float_as_uint(m);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(e, -100) + 127) << 23);
+}
+
+// Brings the codes of the `held` first rows of a page and head from scale s_old to
+// the larger s_new; threads `me` of `team` share the rows.
+__device__ void rescale_rows(uint8_t *codes, int bytes, float ratio, int me, int team)
+{
+    for (int i = me * 16; i < bytes; i += team * 16) {
+        uint4 w = *reinterpret_cast<const uint4 *>(codes + i);
+        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t f = e4m3x2_f16x2((x[j] >> (16 * h)) & 0xffffu);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
+                r |= f32x2_e4m3x2(v.x * ratio, v.y * ratio) << (16 * h);
+            }
+            x[j] = r;
+        }
+        *reinterpret_cast<uint4 *>(codes + i) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+}
+
+__device__ __forceinline__ void store_codes(uint8_t *row, int d0, int d1, const float (&x)[16], float inv)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = f32x2_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+               (f32x2_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+    *reinterpret_cast<uint2 *>(row + d0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2 *>(row + d1) = make_uint2(w[2], w[3]);
+}
+
+// Jobs of a token row: heads [0, H) queries, then the cached heads' keys, then their
+// values.  A team (WARP: one warp; else the block) takes the new tokens of one page
+// of one sequence, one (token, slot) for each thread, and `jobs_per` jobs one after
+// the other: the angles are loaded once for all of them.  Each page and head belongs
+// to one team, so no two threads ever write the same scale or codes.
+template <typename E, bool INTER, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) rope_append_kernel(AppendParams p, int slots_per_seq, int jobs_per, int job_chunks, int64_t teams)
+{
+    __shared__ float red[32];
+    const int team = WARP ? 32 : (int)blockDim.x;
+    const int me = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+    const int64_t unit = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    if (WARP && unit >= teams) return;
+    const int chunk = (int)(unit % job_chunks);
+    const int64_t rest = unit / job_chunks;
+    const int slot = (int)(rest % slots_per_seq), b = (int)(rest / slots_per_seq);
+    const int P = p.kv.page, D = p.kv.dim, SL = D / 16, G = p.kv.kv_heads;
+
+    const Seq sq = load_seq(p.pb, P, b, p.err);
+    if (sq.n == 0) return;
+    // tokens of this team: those of page j of the sequence (page 0 also gets the
+    // tokens below position 0, which are not stored)
+    const int first = max(sq.pos0, 0) >> p.kv.log2_page;
+    const int j = first + slot;
+    const int lo = max(max(sq.pos0, 0), j << p.kv.log2_page), hi = min(sq.len, (j + 1) << p.kv.log2_page);
+    // rows of queries that have no position: zero
+    if (slot == 0 && sq.pos0 < 0 && sq.pos0 + sq.n > sq.pos0) {
+        const int none = min(sq.n, -sq.pos0);
+        E *qo = reinterpret_cast<E *>(p.qo);
+        const int64_t vecs = (int64_t)none * p.heads * (D / 8);
+        if (chunk == 0)
+            for (int64_t i = me; i < vecs; i += team) {
+                const int64_t t = i / (p.heads * (D / 8));
+                const int r = (int)(i % (p.heads * (D / 8)));
+                const float z[16] = {};
+                store8(qo + (sq.t0 + t) * p.qo_st + (r / (D / 8)) * p.qo_sh + (r % (D / 8)) * 8, z, 0);
+            }
+    }
+    if (lo >= hi) return;
+    const int64_t page = checked_page(__ldg(p.pb.table + (int64_t)b * p.pb.table_stride + j), p.kv, p.err);
+    const int items = (hi - lo) * SL;
+    const bool live = me < items;
+    const int pos = lo + me / SL, s = me % SL;
+    const int64_t t = sq.t0 + (pos - sq.pos0);
+    int d0, d1;
+    slot_runs<INTER>(s, p.rot, d0, d1);
+    const bool turn = 16 * s < p.rot;
+    float c[8], sn[8];
+    if (live && turn) {
+        int64_t at = pos;
+        if (at >= p.positions) {
+            *(volatile int *)p.err = CAAT_ERR_INVALID_ARG;
+            at = 0;
+        }
+        const float4 *cp = reinterpret_cast<const float4 *>(p.cos + at * (p.rot / 2) + 8 * s);
+        const float4 *sp = reinterpret_cast<const float4 *>(p.sin + at * (p.rot / 2) + 8 * s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 a = __ldg(cp + i), e = __ldg(sp + i);
+            c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
+            sn[4 * i] = e.x, sn[4 * i + 1] = e.y, sn[4 * i + 2] = e.z, sn[4 * i + 3] = e.w;
+        }
+    }
+    const int job_lo = chunk * jobs_per, job_hi = min(job_lo + jobs_per, p.heads + 2 * G);
+    for (int job = job_lo; job < job_hi; ++job) {
+        const int kind = job < p.heads ? 0 : job < p.heads + G ? 1 : 2;
+        const int h = kind == 0 ? job : (job - p.heads) % G;
+        const E *src = kind == 0 ? reinterpret_cast<const E *>(p.q) + t * p.q_st + (h / p.group) * p.q_sk +
+                                       (h % p.group) * p.q_sg
+                     : kind == 1 ? reinterpret_cast<const E *>(p.k) + t * p.k_st + h * p.k_sh
+                                 : reinterpret_cast<const E *>(p.v) + t * p.v_st + h * p.v_sh;
+        float x[16];
+        if (live) {
+            load8(src + d0, x, 0);
+            load8(src + d1, x, 8);
+            if (kind != 2 && turn) rotate16<INTER>(x, c, sn);
+        }
+        if (kind == 0) {
+            if (live) {
+                E *o = reinterpret_cast<E *>(p.qo) + t * p.qo_st + h * p.qo_sh;
+                store8(o + d0, x, 0);
+                store8(o + d1, x, 8);
+            }
+            continue;
+        }
+        if (page < 0) continue;                       // same for the whole team
+        float m = live ? amax16(x) : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!WARP) {
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+            __syncthreads();
+            m = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        float *scale = (kind == 1 ? p.kv.ks : p.kv.vs) + page * p.kv.scale_stride + h;
+        uint8_t *codes = (kind == 1 ? p.kv.k : p.kv.v) + page * p.kv.page_stride + (int64_t)h * P * D;
+        const int held = lo - (j << p.kv.log2_page);
+        const float s_old = held > 0 ? *(volatile const float *)scale : 0.f;
+        const float s_new = fmaxf(s_old, pow2_scale(m));
+        if (held > 0 && s_new > s_old) rescale_rows(codes, held * D, s_old / s_new, me, team);
+        if (live) store_codes(codes + (int64_t)(pos & (P - 1)) * D, d0, d1, x, 1.f / s_new);
+        // every thread of the team has read the old scale before it changes
+        if (WARP) __syncwarp();
+        else __syncthreads();
+        if (me == 0) *scale = s_new;
+    }
+}
+
+template <typename E, bool INTER>
+caat_status launch(const AppendParams &p, cudaStream_t s)
+{
+    const int P = p.kv.page, SL = p.kv.dim / 16;
+    const int slots = (int)(((int64_t)p.pb.q_max + P - 2) / P + 1);
+    const int jobs = p.heads + 2 * p.kv.kv_heads;
+    const int tokens = p.pb.q_max < P ? p.pb.q_max : P;
+    if (tokens * SL <= 32) {
+        const int64_t teams = (int64_t)p.pb.batch * slots * jobs;
+        const int64_t blocks = (teams + 3) / 4;
+        if (blocks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+        rope_append_kernel<E, INTER, true><<<(unsigned)blocks, 128, 0, s>>>(p, slots, 1, jobs, teams);
+    } else {
+        const int threads = (tokens * SL + 31) / 32 * 32;
+        const int jobs_per = 1, chunks = (jobs + jobs_per - 1) / jobs_per;
+        const int64_t blocks = (int64_t)p.pb.batch * slots * chunks;
+        if (blocks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+        rope_append_kernel<E, INTER, false><<<(unsigned)blocks, threads, 0, s>>>(p, slots, jobs_per, chunks, blocks);
+    }
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    note_launch("rope_append");
+    return CAAT_OK;
+}
+
+}  // namespace
+
+caat_status launch_rope_append(const PagedKV &kv, const PagedBatch &pb, int heads, caat_dtype dt, const void *q,
+                               int64_t q_st, int64_t q_sk, int64_t q_sg, const void *k, int64_t k_st, int64_t k_sh,
+                               const void *v, int64_t v_st, int64_t v_sh, const float *cos, const float *sin,
+                               int64_t positions, int rot, bool interleaved, void *qo, int64_t qo_st, int64_t qo_sh,
+                               cudaStream_t s)
+{
+    AppendParams p{q, k, v, q_st, q_sk, q_sg, k_st, k_sh, v_st, v_sh, qo, qo_st, qo_sh, cos, sin, positions,
+                   heads, heads / kv.kv_heads, rot, serve_error_word(), kv, pb};
+    if (p.err == nullptr) return CAAT_ERR_CUDA;
+    if (dt == CAAT_BF16) return interleaved ? launch<__nv_bfloat16, true>(p, s) : launch<__nv_bfloat16, false>(p, s);
+    return interleaved ? launch<float, true>(p, s) : launch<float, false>(p, s);
+}
+
+}  // namespace caat

@@ -1,0 +1,210 @@
+// C-ABI entry points of the serving operators: argument checks, and the error word
+// that their kernels record bad device-side numbers in.
+#include <initializer_list>
+
+#include "paged.cuh"
+
+namespace caat {
+namespace {
+
+__device__ int g_serve_error;
+
+struct Span { uintptr_t lo, hi; };
+inline bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+
+// bytes of a strided tensor, last dimension dense; sizes and strides in elements
+Span span_of(const void *p, int64_t es, int64_t last, std::initializer_list<int64_t> n, std::initializer_list<int64_t> st)
+{
+    int64_t far = 0;
+    auto s = st.begin();
+    for (const int64_t k : n) {
+        if (k <= 0) return {0, 0};
+        far += (k - 1) * *s++;
+    }
+    return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)((far + last) * es)};
+}
+
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+// non-null, 16-byte aligned, strides non-negative multiples of 16 bytes
+bool good_strided(const void *p, int64_t es, std::initializer_list<int64_t> st)
+{
+    if (p == nullptr || !aligned16(p)) return false;
+    for (const int64_t s : st)
+        if (s < 0 || s > ((int64_t)1 << 48) || (s * es) % 16 != 0) return false;
+    return true;
+}
+
+bool make_kv(const caat_paged_kv *a, PagedKV &kv)
+{
+    if (a == nullptr || a->pages < 1 || a->pages > 0x7fffffff || a->kv_heads < 1 || a->kv_heads > 65536) return false;
+    if (a->page != 16 && a->page != 32 && a->page != 64 && a->page != 128) return false;
+    if (a->dim < 16 || a->dim > 128 || a->dim % 16 != 0) return false;
+    if (a->scale_stride < a->kv_heads || a->scale_stride > ((int64_t)1 << 48)) return false;
+    if (a->page_stride < (int64_t)a->kv_heads * a->page * a->dim) return false;
+    if (!good_strided(a->k, 1, {a->page_stride}) || !good_strided(a->v, 1, {a->page_stride})) return false;
+    if (a->k_scale == nullptr || a->v_scale == nullptr) return false;
+    const int log2_page = a->page == 16 ? 4 : a->page == 32 ? 5 : a->page == 64 ? 6 : 7;
+    kv = PagedKV{(uint8_t *)a->k, (uint8_t *)a->v, a->k_scale, a->v_scale, a->page_stride, a->scale_stride,
+                 a->pages, a->kv_heads, a->page, log2_page, a->dim};
+    return true;
+}
+
+bool make_batch(const caat_paged_batch *a, const PagedKV &kv, PagedBatch &pb)
+{
+    if (a == nullptr || a->batch < 0 || a->tokens < 0 || a->tokens > 0x7fffffff || a->q_max < 0) return false;
+    if (a->table_width < 0 || a->table_stride < a->table_width) return false;
+    // positions are 32-bit, and a tile's last key is counted past the table's end
+    if ((int64_t)a->table_width * kv.page > 0x7fffffff - 1024) return false;
+    if (a->batch > 0 && (a->q_start == nullptr || a->kv_len == nullptr)) return false;
+    if (a->batch > 0 && a->table_width > 0 && a->page_table == nullptr) return false;
+    pb = PagedBatch{a->page_table, a->q_start, a->kv_len, a->table_stride, a->tokens, a->batch, a->table_width, a->q_max};
+    return true;
+}
+
+// the four parts of a cache
+void cache_spans(const PagedKV &kv, Span (&s)[4])
+{
+    const int64_t row = (int64_t)kv.kv_heads * kv.page * kv.dim;
+    s[0] = span_of(kv.k, 1, row, {kv.pages}, {kv.page_stride});
+    s[1] = span_of(kv.v, 1, row, {kv.pages}, {kv.page_stride});
+    s[2] = span_of(kv.ks, 4, kv.kv_heads, {kv.pages}, {kv.scale_stride});
+    s[3] = span_of(kv.vs, 4, kv.kv_heads, {kv.pages}, {kv.scale_stride});
+}
+
+}  // namespace
+
+int *serve_error_word()
+{
+    // one address for each device; the symbol's address never changes
+    static int *cached[128];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return nullptr;
+    int *p = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
+    if (p == nullptr) {
+        if (cudaGetSymbolAddress((void **)&p, g_serve_error) != cudaSuccess) return nullptr;
+        __atomic_store_n(&cached[dev], p, __ATOMIC_RELEASE);
+    }
+    return p;
+}
+
+caat_status read_and_clear_serve_error()
+{
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_serve_error, sizeof(int)) != cudaSuccess) return CAAT_ERR_CUDA;
+    if (v == 0) return CAAT_OK;
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_serve_error, &zero, sizeof(int)) != cudaSuccess) return CAAT_ERR_CUDA;
+    return (caat_status)v;
+}
+
+}  // namespace caat
+
+using namespace caat;
+
+extern "C" caat_status caat_rope_append(const caat_paged_kv *kv_, const caat_paged_batch *batch, int heads,
+                                        caat_dtype dt, const void *q, int64_t q_st, int64_t q_sk, int64_t q_sg,
+                                        const void *k, int64_t k_st, int64_t k_sh, const void *v, int64_t v_st,
+                                        int64_t v_sh, const float *cos, const float *sin, int64_t positions, int rot,
+                                        int interleaved, void *q_out, int64_t qo_st, int64_t qo_sh,
+                                        caat_stream_t stream)
+{
+    PagedKV kv;
+    PagedBatch pb;
+    if ((dt != CAAT_F32 && dt != CAAT_BF16) || !make_kv(kv_, kv) || !make_batch(batch, kv, pb)) return CAAT_ERR_INVALID_ARG;
+    if (heads < 1 || heads > 65536 || heads % kv.kv_heads != 0) return CAAT_ERR_INVALID_ARG;
+    if (rot < 0 || rot > kv.dim || rot % 16 != 0) return CAAT_ERR_INVALID_ARG;
+    if (pb.batch == 0 || pb.tokens == 0 || pb.q_max == 0) return CAAT_OK;
+    if (rot > 0 && (positions < 1 || cos == nullptr || sin == nullptr || !aligned16(cos) || !aligned16(sin)))
+        return CAAT_ERR_INVALID_ARG;
+    const int64_t es = dt == CAAT_BF16 ? 2 : 4, T = pb.tokens, D = kv.dim, G = kv.kv_heads, g = heads / G;
+    if (!good_strided(q, es, {q_st, q_sk, q_sg}) || !good_strided(k, es, {k_st, k_sh}) ||
+        !good_strided(v, es, {v_st, v_sh}) || !good_strided(q_out, es, {qo_st, qo_sh}))
+        return CAAT_ERR_INVALID_ARG;
+    // rows of the output must not share memory: heads within a token, or tokens within a head
+    if ((heads > 1 && qo_sh < D) || (T > 1 && qo_st < D) ||
+        (heads > 1 && T > 1 && qo_st < (heads - 1) * qo_sh + D && qo_sh < (T - 1) * qo_st + D))
+        return CAAT_ERR_INVALID_ARG;
+    const Span sq = span_of(q, es, D, {T, G, g}, {q_st, q_sk, q_sg}), so = span_of(q_out, es, D, {T, heads}, {qo_st, qo_sh});
+    const Span in[7] = {span_of(k, es, D, {T, G}, {k_st, k_sh}),
+                        span_of(v, es, D, {T, G}, {v_st, v_sh}),
+                        span_of(cos, 4, positions * (rot / 2), {1}, {0}),
+                        span_of(sin, 4, positions * (rot / 2), {1}, {0}),
+                        span_of(pb.table, 4, pb.width, {pb.batch}, {pb.table_stride}),
+                        span_of(pb.q_start, 4, pb.batch + 1, {1}, {0}),
+                        span_of(pb.kv_len, 4, pb.batch, {1}, {0})};
+    const bool same = q == q_out && q_st == qo_st && q_sk == g * qo_sh && (g == 1 || q_sg == qo_sh);
+    Span c[4];
+    cache_spans(kv, c);
+    // in-place queries may be parts of one fused row with k and v: the tensors' spans
+    // then overlap, but not the parts of a row, which all lie within one token stride
+    const Span rq = span_of(q, es, D, {G, g}, {q_sk, q_sg}), rk = span_of(k, es, D, {G}, {k_sh}),
+               rv = span_of(v, es, D, {G}, {v_sh});
+    const uintptr_t row_lo = rq.lo < rk.lo ? (rq.lo < rv.lo ? rq.lo : rv.lo) : (rk.lo < rv.lo ? rk.lo : rv.lo);
+    const uintptr_t row_hi = rq.hi > rk.hi ? (rq.hi > rv.hi ? rq.hi : rv.hi) : (rk.hi > rv.hi ? rk.hi : rv.hi);
+    const bool fused = same && q_st == k_st && q_st == v_st && !overlap(rq, rk) && !overlap(rq, rv) &&
+                       row_hi - row_lo <= (uintptr_t)(q_st * es);
+    if (!same && overlap(so, sq)) return CAAT_ERR_INVALID_ARG;
+    for (int i = 0; i < 7; ++i)
+        if (overlap(so, in[i]) && !(fused && i < 2)) return CAAT_ERR_INVALID_ARG;
+    for (int a = 0; a < 4; ++a) {
+        if (overlap(c[a], so) || overlap(c[a], sq)) return CAAT_ERR_INVALID_ARG;
+        for (int i = 0; i < 7; ++i)
+            if (overlap(c[a], in[i])) return CAAT_ERR_INVALID_ARG;
+    }
+    return launch_rope_append(kv, pb, heads, dt, q, q_st, q_sk, q_sg, k, k_st, k_sh, v, v_st, v_sh, cos, sin,
+                              positions, rot, interleaved != 0, q_out, qo_st, qo_sh, (cudaStream_t)stream);
+}
+
+extern "C" caat_status caat_paged_attention(const caat_paged_kv *kv_, const caat_paged_batch *batch, int heads,
+                                            caat_dtype dt, const void *q, int64_t q_st, int64_t q_sk, int64_t q_sg,
+                                            float scale, int window, int sinks, void *out, int64_t o_st, int64_t o_sh,
+                                            caat_stream_t stream)
+{
+    PagedKV kv;
+    PagedBatch pb;
+    if ((dt != CAAT_F32 && dt != CAAT_BF16) || !make_kv(kv_, kv) || !make_batch(batch, kv, pb)) return CAAT_ERR_INVALID_ARG;
+    if (heads < 1 || heads > 65536 || heads % kv.kv_heads != 0) return CAAT_ERR_INVALID_ARG;
+    if (!(scale > 0.f && scale <= 3.402823466e38f) || window < 0 || sinks < 0) return CAAT_ERR_INVALID_ARG;
+    if (pb.batch == 0 || pb.tokens == 0 || pb.q_max == 0) return CAAT_OK;
+    const int64_t es = dt == CAAT_BF16 ? 2 : 4, T = pb.tokens, D = kv.dim, G = kv.kv_heads, g = heads / G;
+    if (!good_strided(q, es, {q_st, q_sk, q_sg}) || !good_strided(out, es, {o_st, o_sh})) return CAAT_ERR_INVALID_ARG;
+    if ((heads > 1 && o_sh < D) || (T > 1 && o_st < D) ||
+        (heads > 1 && T > 1 && o_st < (heads - 1) * o_sh + D && o_sh < (T - 1) * o_st + D))
+        return CAAT_ERR_INVALID_ARG;
+    const Span so = span_of(out, es, D, {T, heads}, {o_st, o_sh});
+    Span c[4];
+    cache_spans(kv, c);
+    const Span in[4] = {span_of(q, es, D, {T, G, g}, {q_st, q_sk, q_sg}),
+                        span_of(pb.table, 4, pb.width, {pb.batch}, {pb.table_stride}),
+                        span_of(pb.q_start, 4, pb.batch + 1, {1}, {0}), span_of(pb.kv_len, 4, pb.batch, {1}, {0})};
+    for (int i = 0; i < 4; ++i)
+        if (overlap(so, in[i]) || overlap(so, c[i])) return CAAT_ERR_INVALID_ARG;
+    // a first token beyond every position is no different from all of them
+    if (sinks > 0x7fffffff - 1024) sinks = 0x7fffffff - 1024;
+    return launch_paged_attention(kv, pb, heads, dt, q, q_st, q_sk, q_sg, scale, window, sinks, out, o_st, o_sh,
+                                  (cudaStream_t)stream);
+}
+
+extern "C" caat_status caat_sample_tokens(int64_t batch, int64_t vocab, caat_dtype dt, const void *logits, int64_t ld,
+                                          const float *u, const float *temperature, const int32_t *top_k,
+                                          const float *top_p, const float *min_p, int32_t *token, float *logprob,
+                                          caat_stream_t stream)
+{
+    if ((dt != CAAT_F32 && dt != CAAT_BF16) || batch < 0 || batch > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+    if (vocab < 1 || vocab > 0x7fffffff - 65536 || ld < vocab || ld > ((int64_t)1 << 48)) return CAAT_ERR_INVALID_ARG;
+    if (batch == 0) return CAAT_OK;
+    for (const void *p : {logits, (const void *)u, (const void *)temperature, (const void *)top_k, (const void *)top_p,
+                          (const void *)min_p, (const void *)token, (const void *)logprob})
+        if (p == nullptr) return CAAT_ERR_INVALID_ARG;
+    const int64_t es = dt == CAAT_BF16 ? 2 : 4;
+    const Span in[6] = {span_of(logits, es, vocab, {batch}, {ld}), span_of(u, 4, batch, {1}, {0}),
+                        span_of(temperature, 4, batch, {1}, {0}),  span_of(top_k, 4, batch, {1}, {0}),
+                        span_of(top_p, 4, batch, {1}, {0}),        span_of(min_p, 4, batch, {1}, {0})};
+    const Span st = span_of(token, 4, batch, {1}, {0}), sl = span_of(logprob, 4, batch, {1}, {0});
+    if (overlap(st, sl)) return CAAT_ERR_INVALID_ARG;
+    for (const Span &i : in)
+        if (overlap(st, i) || overlap(sl, i)) return CAAT_ERR_INVALID_ARG;
+    return launch_sample_tokens(batch, vocab, dt, logits, ld, u, temperature, top_k, top_p, min_p, token, logprob,
+                                (cudaStream_t)stream);
+}

@@ -1,0 +1,207 @@
+"""A token step between the tensor-parallel layers: a paged 8-bit key-value cache,
+the rotary append that fills it, attention over it, and sampling of the next token.
+
+Like the rest of the binding, every function marshals tensors into one library call
+(``include/caat.h``); the arithmetic runs in the library's CUDA kernels.  Two handles
+hold what does not change from call to call, checked once: ``PagedKVCache`` (the cache
+of a layer) and ``PagedBatch`` (the sequences of a step, shared by all its layers).
+"""
+import ctypes
+
+from . import _check, _dtype_code, _lib, _stream_ptr, _torch
+
+
+def _strides(x, last, shape, dtype, name):
+    """Strides of a CUDA tensor of that shape and dtype whose last dimension is dense."""
+    if tuple(x.shape) != shape or x.dtype != dtype or not x.is_cuda:
+        raise ValueError("caat: %s must be a CUDA tensor %s of dtype %s" % (name, list(shape), dtype))
+    st = x.stride()
+    if st[-1] != 1 and last > 1:
+        raise ValueError("caat: the last dimension of %s must be dense" % name)
+    return st
+
+
+def _vector(x, n, dtype, name):
+    if x.dtype != dtype or tuple(x.shape) != (n,) or not x.is_cuda or (n > 1 and x.stride(0) != 1):
+        raise ValueError("caat: %s must be a dense CUDA tensor [%d] of dtype %s" % (name, n, dtype))
+    return ctypes.c_void_p(x.data_ptr())
+
+
+class PagedKVCache:
+    """The cache of one layer: ``k`` and ``v`` float8_e4m3fn [pages, kv_heads, page, dim]
+    (a page may be a slice of a larger tensor; its last three dimensions are dense),
+    ``k_scale`` and ``v_scale`` float32 [pages, kv_heads].  A cached value is code *
+    scale; scales are powers of two.  page: 16, 32, 64 or 128 tokens; dim: a multiple of
+    16 up to 128.  Pages need no initial value: a sequence's first token in a page sets
+    its scale."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        if k.dim() != 4:
+            raise ValueError("caat: k must be [pages, kv_heads, page, dim]")
+        pages, heads, page, dim = k.shape
+        if page not in (16, 32, 64, 128):
+            raise ValueError("caat: a page holds 16, 32, 64 or 128 tokens, not %d" % page)
+        if dim % 16 or not 16 <= dim <= 128:
+            raise ValueError("caat: the head dimension must be a multiple of 16 up to 128, not %d" % dim)
+        for x, name in ((k, "k"), (v, "v")):
+            if tuple(x.shape) != tuple(k.shape) or x.dtype != torch.float8_e4m3fn or not x.is_cuda:
+                raise ValueError("caat: %s must be a CUDA tensor %s of dtype torch.float8_e4m3fn" % (name, list(k.shape)))
+            if x.stride()[1:] != (page * dim, dim, 1) or x.stride(0) != k.stride(0):
+                raise ValueError("caat: the last three dimensions of %s must be dense, and k and v of one page stride" % name)
+        for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if tuple(x.shape) != (pages, heads) or x.dtype != torch.float32 or not x.is_cuda:
+                raise ValueError("caat: %s must be a CUDA tensor [%d, %d] of dtype torch.float32" % (name, pages, heads))
+            if (heads > 1 and x.stride(1) != 1) or x.stride(0) != k_scale.stride(0):
+                raise ValueError("caat: rows of %s must be dense, and k_scale and v_scale of one row stride" % name)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page, self.dim = pages, heads, page, dim
+        self._c = _lib.PagedKV(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                               k.stride(0) if pages > 1 else heads * page * dim,
+                               k_scale.stride(0) if pages > 1 else heads, heads, page, dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages, kv_heads, page, dim, device="cuda"):
+        """A cache of its own storage."""
+        torch = _torch()
+        k, v = (torch.empty(pages, kv_heads, page, dim, dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+        ks, vs = (torch.empty(pages, kv_heads, dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+class PagedBatch:
+    """The sequences of a step.  The new tokens of all sequences lie one after the other
+    in the packed tensors: rows q_start[b] .. q_start[b + 1] - 1 belong to sequence b and
+    take the last places of its kv_len[b] cached tokens (kv_len counts the new ones).
+    page_table: int32 [batch, width], the pages of each sequence in order; q_start: int32
+    [batch + 1]; kv_len: int32 [batch]; q_max: the most new tokens of any sequence.  The
+    tensors are read when a call runs on the GPU, so a captured step may be replayed with
+    new numbers in them.  Numbers that do not fit the buffers are caught on the device
+    (``device_status``), not here."""
+
+    def __init__(self, page_table, q_start, kv_len, q_max):
+        torch = _torch()
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_cuda:
+            raise ValueError("caat: page_table must be a CUDA tensor [batch, width] of dtype torch.int32")
+        batch, width = page_table.shape
+        if width > 1 and page_table.stride(1) != 1:
+            raise ValueError("caat: rows of page_table must be dense")
+        if q_max < 0:
+            raise ValueError("caat: q_max must be >= 0")
+        qs = _vector(q_start, batch + 1, torch.int32, "q_start")
+        kl = _vector(kv_len, batch, torch.int32, "kv_len")
+        self.page_table, self.q_start, self.kv_len, self.q_max, self.batch = page_table, q_start, kv_len, int(q_max), batch
+        self._c = _lib.PagedBatch(page_table.data_ptr(), qs, kl, page_table.stride(0) if batch > 1 else width, 0,
+                                  batch, width, int(q_max))
+        self._ref = ctypes.byref(self._c)
+
+
+def _queries(q, cache):
+    """(tokens, heads, token stride, cached-head stride, group stride) of queries
+    [tokens, heads, dim] or [tokens, kv_heads, heads / kv_heads, dim]."""
+    if not q.is_cuda:
+        raise ValueError("caat: q must be a CUDA tensor")
+    st = q.stride()
+    if q.dim() == 3:
+        T, H, D = q.shape
+        g = H // cache.kv_heads if H % cache.kv_heads == 0 else 0
+        out = T, H, st[0], g * st[1], st[1]
+    elif q.dim() == 4:
+        T, G, g, D = q.shape
+        if G != cache.kv_heads:
+            raise ValueError("caat: q has %d cached heads, the cache %d" % (G, cache.kv_heads))
+        H = G * g
+        out = T, H, st[0], st[1], st[2]
+    else:
+        raise ValueError("caat: q must be [tokens, heads, dim] or [tokens, kv_heads, heads / kv_heads, dim]")
+    if D != cache.dim or g < 1:
+        raise ValueError("caat: q %s does not fit a cache of %d heads of %d" % (list(q.shape), cache.kv_heads, cache.dim))
+    if st[-1] != 1:
+        raise ValueError("caat: the last dimension of q must be dense")
+    return out
+
+
+def rope_append(q, k, v, cos, sin, cache, batch, interleaved=False, q_out=None, stream=None):
+    """Rotates the new queries and keys, and writes keys and values into ``cache``.
+
+    q: [tokens, heads, dim] (or [tokens, kv_heads, heads / kv_heads, dim]); k, v: [tokens,
+    kv_heads, dim]; bf16 or fp32, strided views welcome (16-byte aligned).  cos, sin:
+    float32 [positions, rot / 2]: the first rot values of a head are turned by the angles
+    of the token's position, in pairs (2i, 2i + 1) if interleaved, else (i, i + rot / 2);
+    None: no rotation.  Returns the rotated queries [tokens, heads, dim] (``q_out``, which
+    may be ``q``, allocated when None)."""
+    torch = _torch()
+    T, H, q_st, q_sk, q_sg = _queries(q, cache)
+    kst = _strides(k, cache.dim, (T, cache.kv_heads, cache.dim), q.dtype, "k")
+    vst = _strides(v, cache.dim, (T, cache.kv_heads, cache.dim), q.dtype, "v")
+    dt = _dtype_code(q)
+    if (cos is None) != (sin is None):
+        raise ValueError("caat: cos and sin are given together")
+    positions, rot, cp, sp = 0, 0, None, None
+    if cos is not None:
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        for x, name in ((cos, "cos"), (sin, "sin")):
+            if tuple(x.shape) != (positions, rot // 2) or x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
+                raise ValueError("caat: %s must be a dense CUDA tensor [positions, rot / 2] of dtype torch.float32" % name)
+        cp, sp = ctypes.c_void_p(cos.data_ptr()), ctypes.c_void_p(sin.data_ptr())
+    if q_out is None:
+        q_out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
+    ost = _strides(q_out, cache.dim, (T, H, cache.dim), q.dtype, "q_out")
+    batch._c.tokens = T
+    st = _lib.load().caat_rope_append(
+        cache._ref, batch._ref, H, dt, ctypes.c_void_p(q.data_ptr()), q_st, q_sk, q_sg,
+        ctypes.c_void_p(k.data_ptr()), kst[0], kst[1], ctypes.c_void_p(v.data_ptr()), vst[0], vst[1],
+        cp, sp, positions, rot, 1 if interleaved else 0, ctypes.c_void_p(q_out.data_ptr()), ost[0], ost[1],
+        _stream_ptr(stream, q))
+    _check(st, "caat_rope_append")
+    return q_out
+
+
+def paged_attention(q, cache, batch, softmax_scale=None, window=0, sinks=0, out=None, stream=None):
+    """Softmax attention of the new tokens over the cache.
+
+    q: rotated queries, shaped as for ``rope_append``.  The query at position p sees the
+    cached keys j <= p; with window > 0 only j > p - window and j < sinks (the first tokens
+    stay visible).  softmax_scale: 1 / sqrt(dim) when None.  Returns [tokens, heads, dim]
+    of q's dtype (``out``, allocated when None); a query that sees nothing gives zeros."""
+    torch = _torch()
+    T, H, q_st, q_sk, q_sg = _queries(q, cache)
+    dt = _dtype_code(q)
+    if out is None:
+        out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
+    ost = _strides(out, cache.dim, (T, H, cache.dim), q.dtype, "out")
+    batch._c.tokens = T
+    st = _lib.load().caat_paged_attention(
+        cache._ref, batch._ref, H, dt, ctypes.c_void_p(q.data_ptr()), q_st, q_sk, q_sg,
+        cache.dim ** -0.5 if softmax_scale is None else float(softmax_scale), int(window), int(sinks),
+        ctypes.c_void_p(out.data_ptr()), ost[0], ost[1], _stream_ptr(stream, q))
+    _check(st, "caat_paged_attention")
+    return out
+
+
+def sample_tokens(logits, u, temperature, top_k, top_p, min_p, tokens=None, logprobs=None, stream=None):
+    """The next token of each row of logits [batch, vocab] (bf16 or fp32).
+
+    u: float32 [batch], uniform in [0, 1); temperature (<= 0: the largest logit), top_p
+    (>= 1: off), min_p (0: off): float32 [batch]; top_k (<= 0: off): int32 [batch].  The
+    filters apply in the order temperature, top-k, top-p, min-p; equal logits count by
+    index, lowest first.  Returns (tokens int32 [batch], logprobs float32 [batch]: log
+    softmax(logits) of each token, before temperature and filters).  A row without a
+    logit above -inf gives -1 and -inf."""
+    torch = _torch()
+    if logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("caat: logits must be a CUDA tensor [batch, vocab] with dense rows")
+    B, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    if tokens is None:
+        tokens = torch.empty(B, dtype=i32, device=logits.device)
+    if logprobs is None:
+        logprobs = torch.empty(B, dtype=f32, device=logits.device)
+    st = _lib.load().caat_sample_tokens(
+        B, V, _dtype_code(logits), ctypes.c_void_p(logits.data_ptr()), logits.stride(0) if B > 1 else V,
+        _vector(u, B, f32, "u"), _vector(temperature, B, f32, "temperature"), _vector(top_k, B, i32, "top_k"),
+        _vector(top_p, B, f32, "top_p"), _vector(min_p, B, f32, "min_p"), _vector(tokens, B, i32, "tokens"),
+        _vector(logprobs, B, f32, "logprobs"), _stream_ptr(stream, logits))
+    _check(st, "caat_sample_tokens")
+    return tokens, logprobs
