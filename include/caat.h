@@ -557,7 +557,7 @@ caat_status caat_paged_attention(const caat_paged_kv *kv, const caat_paged_batch
  * lowest index of equals.  temperature, top_k (int32), top_p, min_p: device arrays of
  * batch numbers.  token: int32[batch]; logprob: fp32[batch], log softmax(z) of the
  * token, before temperature and filters.  NaN counts as -inf; a row of nothing else
- * gives token -1 and logprob -inf.  vocab < 2^31.  Errors: INVALID_ARG.
+ * gives token -1 and logprob -inf.  vocab is at most 2^22.  Errors: INVALID_ARG.
  */
 caat_status caat_sample_tokens(int64_t batch, int64_t vocab, caat_dtype dt, const void *logits, int64_t ld,
                                const float *u, const float *temperature, const int32_t *top_k, const float *top_p,

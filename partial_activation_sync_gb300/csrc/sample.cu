@@ -10,17 +10,34 @@
 // first of the order is always kept.  The log probability returned is the token's
 // under softmax(z), before temperature and filters.
 //
-// Every filter keeps a prefix of the order, so together they are one threshold: a
-// value and how many of its equals stay.  Nothing is sorted: the threshold is found by
-// bisection over the 32-bit ordered form of the values, each step one pass over the
-// row for a count or a sum of weights.  Weights are summed in fp32 over at most a few
-// hundred terms and then in 64 bits, in a fixed order.
+// Every filter keeps a prefix of the order, so together they are one threshold: the
+// last token kept.  The row is never sorted; what is sorted, in shared memory, is a few
+// hundred candidates.
+//  - top-k: the k-th largest of the threads' own maxima bounds the k-th largest logit
+//    from below, and little more than k logits lie above it;
+//  - top-p alone: two histogram passes find the narrow interval in which the prefix ends:
+//    32 bins over the gap to the largest logit, four to an octave, then 32 equal parts of
+//    the bin where the weight is reached.  Each lane has its own bins (a column of shared
+//    memory: no atomics, no bank conflicts, a fixed order of every sum);
+//  - rows with more candidates than the list holds, as when most logits are equal, take
+//    bisection over the ordered values, one pass for each step.
+// Sums beyond a thread's are 64-bit integers in units of 2^-40 of the largest weight:
+// exact in any order, and the chip's fp64 rate is too low for the short chains between
+// the passes.
+//
+// One block for a row, each warp on one run of it, so that the sums of the runs say
+// where the drawn token lies.  The passes after the first find the row in L2 or L1.
+// Bound by the instructions of those passes for large vocabularies and by the latency
+// of the chain for few rows.
 #include "paged.cuh"
 
 namespace caat {
 namespace {
 
-constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = 32;
+constexpr int CAP = 2048;                       // values that are sorted in shared memory
+constexpr float FLT_BIG = 3.402823466e38f;
+constexpr float LOG2E = 1.4426950408889634f;
 
 struct SampleParams {
     const void *logits;
@@ -46,65 +63,216 @@ __device__ __forceinline__ float unordered(uint32_t k)
 
 constexpr uint32_t KEY_NEG_INF = 0x007fffffu;   // ordered(-inf)
 
-__device__ __forceinline__ float value(const float *p, int64_t i) { return __ldg(p + i); }
-__device__ __forceinline__ float value(const __nv_bfloat16 *p, int64_t i)
+__device__ __forceinline__ float value(const float *p, int i) { return __ldg(p + i); }
+__device__ __forceinline__ float value(const __nv_bfloat16 *p, int i)
 {
     return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p) + i) << 16);
 }
 
+// f(index, logit) for every element of [lo, hi), shared out over `team` threads: 16-byte
+// loads, four in flight, between an unaligned head and tail.  Threads call f a different
+// number of times.
+template <typename E, typename F>
+__device__ __forceinline__ void each(const E *z, int lo, int hi, int me, int team, F f)
+{
+    constexpr int N = 16 / sizeof(E), U = 4;
+    const int off = (int)(((16 - ((uintptr_t)(z + lo) & 15)) & 15) / sizeof(E));
+    const int a = min(hi, lo + off), vecs = (hi - a) / N, b = a + vecs * N;
+    for (int i = lo + me; i < a; i += team) f(i, value(z, i));
+    const uint4 *v = reinterpret_cast<const uint4 *>(z + a);
+    for (int i = me; i < vecs; i += U * team) {
+        uint4 w[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i + k * team < vecs) w[k] = __ldg(v + i + k * team);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i + k * team >= vecs) break;
+            const int at = a + (i + k * team) * N;
+            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (N == 8) {
+                    f(at + 2 * e, __uint_as_float(x[e] << 16));
+                    f(at + 2 * e + 1, __uint_as_float(x[e] & 0xffff0000u));
+                } else {
+                    f(at + e, __uint_as_float(x[e]));
+                }
+            }
+        }
+    }
+    for (int i = b + me; i < hi; i += team) f(i, value(z, i));
+}
+
+typedef unsigned long long u64;
+
 struct Shared {
-    double d[WARPS];
-    unsigned long long l[WARPS];
-    double bd;
-    unsigned long long bl;
+    u64 list[CAP];
+    float bins[WARPS][BINS][32];
+    u64 total[BINS];
+    u64 l[WARPS];
+    u64 bl;
+    int n;
 };
 
-__device__ __forceinline__ double block_sum(double x, Shared &sh)
+constexpr float ONE = 1099511627776.f;          // 2^40: a weight of 1
+
+__device__ __forceinline__ u64 fixed(float w) { return (u64)(w * ONE); }
+
+__device__ __forceinline__ u64 block_sum(u64 x, Shared &sh)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.d[threadIdx.x >> 5] = x;
+    if ((threadIdx.x & 31) == 0) sh.l[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = sh.d[threadIdx.x & 31];
+    x = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return __shfl_sync(0xffffffffu, x, 0);
 }
 
-__device__ __forceinline__ unsigned long long block_max(unsigned long long x, Shared &sh)
+// sum of the values of the threads below this one, and of all
+__device__ __forceinline__ u64 block_scan(u64 x, Shared &sh, u64 &all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.l[warp] = inc;
+    __syncthreads();
+    u64 below = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        const u64 y = sh.l[w];
+        if (w < warp) below += y;
+        all += y;
+    }
+    return below + inc - x;
+}
+
+__device__ __forceinline__ u64 block_max(u64 x, Shared &sh)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.l[threadIdx.x >> 5] = x;
     __syncthreads();
-    x = sh.l[threadIdx.x & 31];
+    x = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+    for (int o = 8; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return __shfl_sync(0xffffffffu, x, 0);
 }
 
-template <typename E>
-__global__ void __launch_bounds__(THREADS) sample_kernel(SampleParams p)
+// sh.list[0, n) largest first (bitonic; n is padded to a power of two with zeros)
+__device__ __noinline__ void sort_list(Shared &sh, int n)
 {
-    __shared__ Shared sh;
+    int m = 2;
+    while (m < n) m *= 2;
+    for (int i = n + threadIdx.x; i < m; i += THREADS) sh.list[i] = 0;
+    for (int k = 2; k <= m; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            __syncthreads();
+            for (int p = threadIdx.x; p < m / 2; p += THREADS) {
+                const int i = 2 * p - (p & (j - 1)), q = i + j;
+                const u64 a = sh.list[i], b = sh.list[q];
+                if ((a < b) == ((i & k) == 0)) {
+                    sh.list[i] = b;
+                    sh.list[q] = a;
+                }
+            }
+        }
+    __syncthreads();
+}
+
+// bin of a gap t >= 0: [0, 1/8), then four to an octave up to 24, then the rest
+__device__ __forceinline__ int coarse_bin(float t)
+{
+    return min(max((int)(__float_as_uint(t) >> 21) - (127 - 3) * 4 + 1, 0), BINS - 1);
+}
+__device__ __forceinline__ float coarse_edge(int bin)
+{
+    return bin == 0 ? 0.f : __uint_as_float((uint32_t)((127 - 3) * 4 + bin - 1) << 21);
+}
+
+// The lanes' bins summed into sh.total.
+__device__ void sum_bins(Shared &sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+#pragma unroll
+    for (int b = warp; b < BINS; b += WARPS) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) s += sh.bins[w][b][lane];
+        u64 d = fixed(s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        if (lane == 0) sh.total[b] = d;
+    }
+    __syncthreads();
+}
+
+// The bin where `before` + the running sum first reaches `target` (or the last one with
+// anything in it); `before` becomes the sum up to it.
+__device__ int find_bin(const Shared &sh, u64 target, u64 &before)
+{
+    int at = 0;
+    u64 sum = before, upto = before;
+    for (int b = 0; b < BINS; ++b) {
+        const u64 x = sh.total[b];
+        if (x > 0) {
+            at = b;
+            upto = sum;
+            if (sum + x >= target) break;
+        }
+        sum += x;
+    }
+    before = upto;
+    return at;
+}
+
+__device__ __forceinline__ void clear_bins(Shared &sh)
+{
+    __syncthreads();
+    float *b = &sh.bins[threadIdx.x >> 5][0][threadIdx.x & 31];
+#pragma unroll
+    for (int i = 0; i < BINS; ++i) b[32 * i] = 0.f;
+    // a lane's column is its own: no barrier
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// share of a 64-bit sum
+__device__ __forceinline__ u64 part_of(float f, u64 sum) { return (u64)((double)f * (double)sum); }
+
+template <typename E>
+__global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(raw);
     const int64_t row = blockIdx.x;
     const E *z = reinterpret_cast<const E *>(p.logits) + row * p.ld;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int V = (int)p.V;
-    // each warp owns one run of the row, so that sums in index order are sums over warps
-    const int seg = (V + WARPS - 1) / WARPS;
-    const int lo = min(V, warp * seg), hi = min(V, lo + seg);
+    const int seg = (V + WARPS - 1) / WARPS, lo = min(V, warp * seg), hi = min(V, lo + seg);   // this warp's run
 
-    // largest value and its lowest index
-    unsigned long long best = 0;
-    for (int i = lo + lane; i < hi; i += 32)
-        best = max(best, (unsigned long long)ordered(value(z, i)) << 32 | (uint32_t)~i);
-    best = block_max(best, sh);
-    const uint32_t kmax = (uint32_t)(best >> 32);
+    // the thread's and the row's largest value (fmaxf passes over NaN)
+    float top = -INFINITY;
+    each(z, lo, hi, lane, 32, [&](int, float x) { top = fmaxf(top, x); });
+    const uint32_t kmax = (uint32_t)block_max(ordered(top), sh);
     if (kmax <= KEY_NEG_INF) {                    // no token can be drawn
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             p.token[row] = -1;
             p.logprob[row] = -INFINITY;
         }
@@ -112,36 +280,219 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(SampleParams p)
     }
     const float zmax = unordered(kmax);
     const float T = p.temperature[row];
-    // equal values weigh 1 even where both are infinite; -inf, NaN and all below +inf
-    // weigh 0.  The gap stays finite, so that an infinite T makes it 0 and not NaN.
-    auto weight = [&](float x, float inv) {
-        return x == zmax ? 1.f
-               : x > -INFINITY && zmax < INFINITY ? expf(fmaxf(x - zmax, -3.402823466e38f) * inv) : 0.f;
+    const int k = p.top_k[row];
+    const float tp = p.top_p[row], mp = p.min_p[row];
+    const bool draw = T > 0.f, by_count = draw && k > 0 && k < V, by_weight = draw && !by_count && tp < 1.f;
+    // 1 / T, kept above 0 so that an infinite gap stays infinite
+    const float inv = draw ? fmaxf(1.f / T, 1.4e-45f) : 1.f;
+    // gap to the largest logit: infinite for -inf, NaN and, where the largest is +inf,
+    // for all others; else finite, so that an infinite T makes it 0
+    const float zref = fminf(zmax, FLT_BIG), floor = zmax < INFINITY ? -INFINITY : FLT_BIG;
+    auto gap = [&](float x) { return x > floor ? fminf(fmaxf(zref - x, 0.f), FLT_BIG) : INFINITY; };
+    auto scaled = [&](float g) { return g * inv; };
+    auto weight = [&](float g) { return exp2_approx(-LOG2E * scaled(g)); };
+    float part = 0.f;                             // sum of e^(z - max)
+    auto plain = [&](float g) { part += exp2_approx(-LOG2E * g); };
+
+    int token = -1;
+    // kept: keys above thr, and those equal to it up to index cut; weights from mp on
+    uint32_t thr = 0;
+    int cut = V;
+    auto kept = [&](int i, float x, float g) {
+        const float w = weight(g);
+        const uint32_t key = ordered(x);
+        return key > thr || (key == thr && i < cut) ? (key == kmax || w >= mp ? w : 0.f) : 0.f;
     };
-    float part = 0.f;
-    for (int i = lo + lane; i < hi; i += 32) part += weight(value(z, i), 1.f);
-    const double all = block_sum(part, sh);
-    int token = (int)~(uint32_t)best;
-    if (T > 0.f) {
-        const float inv = 1.f / T;
+    bool slow = false;
+    float runs = 0.f;                             // kept weight of this warp's run, lane by lane
+    bool have_runs = false;
+
+    if (!draw) {
+        int at = 0x7fffffff;
+        each(z, lo, hi, lane, 32, [&](int i, float x) {
+            plain(gap(x));
+            if (x == zmax) at = min(at, i);
+        });
+        token = (int)~(uint32_t)block_max((uint32_t)~at, sh);
+    } else if (by_count) {
+        // a value that k of the threads' maxima reach: at least k logits do, and not many
+        // more.  2 k < THREADS keeps the expected number below 1.4 k (the measured rule:
+        // beyond it the candidates grow as the logarithm, and past CAP they are too many).
+        uint32_t floor_key = 0;
+        if (2 * k < THREADS) {
+            const uint32_t own = ordered(top);
+            uint32_t a = 0, b = kmax;             // count(own >= a) >= k
+            while (a < b) {
+                const uint32_t mid = a + (b - a) / 2 + 1;
+                const int n = __syncthreads_count(own >= mid);
+                if (n >= k) {
+                    a = mid;
+                    if (n <= k + k / 8) break;
+                } else {
+                    b = mid - 1;
+                }
+            }
+            floor_key = a;
+        } else {
+            slow = true;
+        }
+        const float least = unordered(max(floor_key, KEY_NEG_INF));
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+        each(z, lo, hi, lane, 32, [&](int i, float x) {
+            plain(gap(x));
+            if (x >= least && !slow) {
+                const int at = atomicAdd(&sh.n, 1);              // any order: the list is sorted
+                if (at < CAP) sh.list[at] = (u64)ordered(x) << 32 | (uint32_t)~i;
+            }
+        });
+        __syncthreads();
+        int n = sh.n;
+        slow = slow || n > CAP;
+        if (!slow) {
+            sort_list(sh, n);
+            // top-p and min-p in the sorted list; a thread holds PER neighbours
+            constexpr int PER = CAP / THREADS;
+            n = min(n, k);
+            float w[PER];
+            u64 own = 0, sum;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * PER + e;
+                w[e] = i < n ? weight(gap(unordered((uint32_t)(sh.list[i] >> 32)))) : 0.f;
+                own += fixed(w[e]);
+            }
+            u64 run = block_scan(own, sh, sum);
+            const u64 target = tp < 1.f ? part_of(fmaxf(tp, 0.f), sum) : ~0ull;
+            int stay = 0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * PER + e;
+                if (i < n && (i == 0 || (run < target && w[e] >= mp))) stay = i + 1;
+                run += fixed(w[e]);
+            }
+            n = (int)block_max((u64)stay, sh);
+            // the draw among those, in index order
+            u64 at[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * PER + e;
+                at[e] = i < n ? sh.list[i] << 32 | sh.list[i] >> 32 : 0;        // (~index, key)
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (tid * PER + e < n) sh.list[tid * PER + e] = at[e];
+            sort_list(sh, n);
+            own = 0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid * PER + e;
+                w[e] = i < n ? weight(gap(unordered((uint32_t)sh.list[i]))) : 0.f;
+                own += fixed(w[e]);
+            }
+            run = block_scan(own, sh, sum);
+            const u64 t = part_of(p.u[row], sum);
+            int hit = -1, last = -1;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                run += fixed(w[e]);
+                if (w[e] > 0.f) {
+                    last = tid * PER + e;
+                    if (hit < 0 && run > t) hit = last;
+                }
+            }
+            // the lowest place that passes; the last with a weight if rounding leaves none
+            const u64 code = block_max(hit >= 0 ? 2ull * CAP - hit : (u64)(last + 1), sh);
+            token = (int)~(uint32_t)(sh.list[code > CAP ? 2 * CAP - code : code - 1] >> 32);
+        }
+    } else if (by_weight) {
+        float *mine = &sh.bins[warp][0][lane];
+        clear_bins(sh);
+        each(z, lo, hi, lane, 32, [&](int, float x) {
+            const float g = gap(x), t = scaled(g);
+            plain(g);
+            mine[32 * coarse_bin(t)] += exp2_approx(-LOG2E * t);
+        });
+        sum_bins(sh);
+        u64 sum = 0, before = 0;
+#pragma unroll
+        for (int b = 0; b < BINS; ++b) sum += sh.total[b];
+        const u64 target = part_of(fmaxf(tp, 0.f), sum);
+        const int j = find_bin(sh, target, before);
+        slow = j == BINS - 1;
+        if (!slow) {
+            const float from = coarse_edge(j), fine = BINS / (coarse_edge(j + 1) - from);
+            auto sub = [&](float t) { return min(max((int)((t - from) * fine), 0), BINS - 1); };
+            clear_bins(sh);
+            each(z, lo, hi, lane, 32, [&](int, float x) {
+                const float t = scaled(gap(x));
+                if (coarse_bin(t) == j) mine[32 * sub(t)] += exp2_approx(-LOG2E * t);
+            });
+            sum_bins(sh);
+            const int s = find_bin(sh, target, before);
+            if (tid == 0) sh.n = 0;
+            __syncthreads();
+            each(z, lo, hi, lane, 32, [&](int i, float x) {
+                const float t = scaled(gap(x));
+                if (coarse_bin(t) == j && sub(t) == s) {
+                    const int at = atomicAdd(&sh.n, 1);          // any order: the list is sorted
+                    if (at < CAP) sh.list[at] = (u64)ordered(x) << 32 | (uint32_t)~i;
+                }
+            });
+            __syncthreads();
+            int n = sh.n;
+            slow = n > CAP;
+            if (!slow) {
+                sort_list(sh, n);
+                constexpr int PER = CAP / THREADS;
+                float w[PER];
+                u64 own = 0, dummy;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int i = tid * PER + e;
+                    w[e] = i < n ? weight(gap(unordered((uint32_t)(sh.list[i] >> 32)))) : 0.f;
+                    own += fixed(w[e]);
+                }
+                u64 run = before + block_scan(own, sh, dummy);
+                int stay = 0;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int i = tid * PER + e;
+                    if (i < n && (run < target || (before == 0 && i == 0))) stay = i + 1;
+                    run += fixed(w[e]);
+                }
+                n = (int)block_max((u64)stay, sh);
+                // the last token kept; none of the interval if its predecessors suffice
+                const u64 end = sh.list[max(n - 1, 0)];
+                thr = (uint32_t)(end >> 32);
+                cut = (int)~(uint32_t)end + (n > 0);
+            }
+        }
+    } else {
+        each(z, lo, hi, lane, 32, [&](int i, float x) {
+            const float g = gap(x);
+            plain(g);
+            runs += kept(i, x, g);
+        });
+        have_runs = true;
+    }
+    const u64 all = block_sum(fixed(part), sh);
+
+    if (slow) {
+        // bisection over the ordered values
         auto count_ge = [&](uint32_t key) {
             int n = 0;
-            for (int i = lo + lane; i < hi; i += 32) n += ordered(value(z, i)) >= key;
-            return (int64_t)block_sum(n, sh);
+            each(z, lo, hi, lane, 32, [&](int, float x) { n += ordered(x) >= key; });
+            return (int64_t)block_sum((u64)n, sh);
         };
         auto weight_ge = [&](uint32_t key) {
             float s = 0.f;
-            for (int i = lo + lane; i < hi; i += 32) {
-                const float x = value(z, i);
-                if (ordered(x) >= key) s += weight(x, inv);
-            }
-            return block_sum(s, sh);
+            each(z, lo, hi, lane, 32, [&](int, float x) { s += ordered(x) >= key ? weight(gap(x)) : 0.f; });
+            return block_sum(fixed(s), sh);
         };
-        // kept: keys above thr, and the first `ties` of those equal to it
-        uint32_t thr = 0;
-        int64_t ties = V;
-        const int k = p.top_k[row];
-        if (k > 0 && k < V) {
+        int64_t ties = V;                         // how many of those equal to thr stay
+        if (by_count) {
             uint32_t a = 0, b = kmax;             // count_ge(a) >= k; the largest such key
             while (a < b) {
                 const uint32_t mid = a + (b - a) / 2 + 1;
@@ -149,110 +500,115 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(SampleParams p)
                 else b = mid - 1;
             }
             thr = a;
-            ties = thr == 0xffffffffu ? k : k - count_ge(thr + 1);
+            ties = k - count_ge(thr + 1);
         }
-        const float tp = p.top_p[row], mp = p.min_p[row];
-        const float wthr = weight(unordered(thr), inv);
         if (tp < 1.f) {
+            const u64 wthr = fixed(weight(gap(unordered(thr))));
             auto kept_ge = [&](uint32_t key) {    // weight of the kept with keys >= key
                 if (thr == 0) return weight_ge(key);
-                return key > thr ? weight_ge(key) : weight_ge(thr + 1) + (double)ties * wthr;
+                return key > thr ? weight_ge(key) : weight_ge(thr + 1) + (u64)ties * wthr;
             };
-            const double target = (double)tp * kept_ge(0);
+            const u64 target = part_of(fmaxf(tp, 0.f), kept_ge(0));
             uint32_t a = thr, b = kmax;
             while (a < b) {
                 const uint32_t mid = a + (b - a) / 2 + 1;
                 if (kept_ge(mid) >= target) a = mid;
                 else b = mid - 1;
             }
-            const double above = a == 0xffffffffu ? 0.0 : kept_ge(a + 1);
-            const double w = weight(unordered(a), inv);
+            const u64 above = kept_ge(a + 1), w = fixed(weight(gap(unordered(a))));
             // equals i = 0, 1, ... stay while above + i w < target
-            const double n = w > 0.0 ? ceil((target - above) / w) : (above < target ? 4e18 : 0.0);
-            int64_t stay = n < 1.0 ? (a == kmax ? 1 : 0) : n > 4e18 ? (int64_t)4e18 : (int64_t)n;
+            int64_t stay = above >= target ? 0 : w > 0 ? (int64_t)((target - above + w - 1) / w) : V;
+            if (a == kmax && stay < 1) stay = 1;
             if (a != thr || stay < ties) {
                 thr = a;
                 ties = stay;
             }
         }
-        // where the equals that stay end, in index order
-        int cut = V;
         if (ties < V) {
+            // where the equals that stay end, in index order: count them run by run
             int n = 0;
             for (int i = lo + lane; i < hi; i += 32) n += ordered(value(z, i)) == thr;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
             __syncthreads();
-            if (lane == 0) sh.l[warp] = (unsigned long long)n;
-            if (threadIdx.x == 0) sh.bl = (unsigned long long)V;
+            if (lane == 0) sh.l[warp] = (u64)n;
+            if (tid == 0) sh.bl = (u64)V;
             __syncthreads();
             int64_t before = 0;
             for (int w = 0; w < warp; ++w) before += (int64_t)sh.l[w];
-            if (before <= ties && before + n > ties) {       // the first equal that goes is here
+            if (before <= ties && before + n > ties) {           // the first equal that goes is here
                 for (int i0 = lo; i0 < hi; i0 += 32) {
                     const bool eq = i0 + lane < hi && ordered(value(z, i0 + lane)) == thr;
                     const uint32_t m = __ballot_sync(0xffffffffu, eq);
-                    if (eq && before + __popc(m & ((1u << lane) - 1)) == ties) sh.bl = (unsigned long long)(i0 + lane);
+                    if (eq && before + __popc(m & ((1u << lane) - 1)) == ties) sh.bl = (u64)(i0 + lane);
                     before += __popc(m);
                 }
             }
             __syncthreads();
             cut = (int)sh.bl;
         }
-        auto kept = [&](int i) {                  // weight of token i, 0 when it goes
-            const float x = value(z, i);
-            const uint32_t key = ordered(x);
-            if (key < thr || (key == thr && i >= cut)) return 0.f;
-            const float w = weight(x, inv);
-            return key == kmax || w >= mp ? w : 0.f;
-        };
-        float s = 0.f;
-        for (int i = lo + lane; i < hi; i += 32) s += kept(i);
-        double ws = s;
+    }
+    if (token < 0) {
+        // the draw over the row: the sums of the runs say which one holds the answer, and
+        // the block goes through that one thread by thread
+        if (!have_runs) each(z, lo, hi, lane, 32, [&](int i, float x) { runs += kept(i, x, gap(x)); });
+        u64 ws = fixed(runs);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
         __syncthreads();
-        if (lane == 0) sh.d[warp] = ws;
-        if (threadIdx.x == 0) sh.bl = 0;
+        if (lane == 0) sh.l[warp] = ws;
         __syncthreads();
-        double before = 0, total = 0;
-        for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) before += sh.d[w];
-            total += sh.d[w];
-        }
-        const double target = (double)p.u[row] * total;
-        // the last warp with anything kept answers when rounding leaves no prefix above the target
-        if (ws > 0 && before <= target) {
-            int last = -1, found = -1;
-            double run = before;
-            for (int i0 = lo; i0 < hi && found < 0; i0 += 32) {
-                const double w = i0 + lane < hi ? (double)kept(i0 + lane) : 0.0;
-                double inc = w;
+        u64 total = 0;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const uint32_t pos = __ballot_sync(0xffffffffu, w > 0.0);
-                const uint32_t hit = __ballot_sync(0xffffffffu, w > 0.0 && run + inc > target);
-                if (pos) last = i0 + 31 - __clz((int)pos);
-                if (hit) found = i0 + __ffs((int)hit) - 1;
-                run += __shfl_sync(0xffffffffu, inc, 31);
+        for (int w = 0; w < WARPS; ++w) total += sh.l[w];
+        const u64 target = part_of(p.u[row], total);
+        int at = 0;                               // the run: the last with a weight if rounding leaves none
+        u64 before = 0, sum = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            const u64 x = sh.l[w];
+            if (x > 0) {
+                at = w;
+                before = sum;
+                if (sum + x > target) break;
             }
-            // the lowest warp that holds the target wins: it writes its candidate with
-            // the highest rank
-            if (lane == 0)
-                atomicMax(&sh.bl, (unsigned long long)(found >= 0 ? 2 * WARPS - warp : 0) << 32 |
-                                      (uint32_t)(found >= 0 ? found : last));
+            sum += x;
         }
-        __syncthreads();
-        token = (int)(uint32_t)sh.bl;
+        const int first = at * seg, end = min(V, first + seg), per = (end - first + THREADS - 1) / THREADS;
+        const int from = min(end, first + tid * per), to = min(end, from + per);
+        u64 own = 0, dummy;
+        for (int i = from; i < to; ++i) {
+            const float x = value(z, i);
+            own += fixed(kept(i, x, gap(x)));
+        }
+        u64 run = before + block_scan(own, sh, dummy);
+        int hit = -1, last = -1;
+        for (int i = from; i < to && hit < 0; ++i) {
+            const float x = value(z, i), w = kept(i, x, gap(x));
+            run += fixed(w);
+            if (w > 0.f) {
+                last = i;
+                if (run > target) hit = i;
+            }
+        }
+        const u64 big = 1ull << 32, code = block_max(hit >= 0 ? 2 * big - hit : (u64)(last + 1), sh);
+        token = code > big ? (int)(2 * big - code) : (int)code - 1;
     }
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         const float x = value(z, token);
         p.token[row] = token;
-        p.logprob[row] = (float)((x == zmax ? 0.0 : (double)x - (double)zmax) - log(all));
+        p.logprob[row] = (x == zmax ? 0.f : x - zmax) - logf((float)all * (1.f / ONE));
     }
+}
+
+template <typename E>
+caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
+{
+    auto kern = sample_kernel<E>;
+    if (prepare_kernel_smem((const void *)kern, (int)sizeof(Shared)) != CAAT_OK) return CAAT_ERR_CUDA;
+    kern<<<(unsigned)B, THREADS, sizeof(Shared), s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    note_launch("sample_tokens");
+    return CAAT_OK;
 }
 
 }  // namespace
@@ -262,11 +618,7 @@ caat_status launch_sample_tokens(int64_t B, int64_t V, caat_dtype dt, const void
                                  const float *min_p, int32_t *token, float *logprob, cudaStream_t s)
 {
     const SampleParams p{logits, ld, V, u, temperature, top_p, min_p, top_k, token, logprob};
-    if (dt == CAAT_BF16) sample_kernel<__nv_bfloat16><<<(unsigned)B, THREADS, 0, s>>>(p);
-    else sample_kernel<float><<<(unsigned)B, THREADS, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
-    note_launch("sample_tokens");
-    return CAAT_OK;
+    return dt == CAAT_BF16 ? launch<__nv_bfloat16>(B, p, s) : launch<float>(B, p, s);
 }
 
 }  // namespace caat

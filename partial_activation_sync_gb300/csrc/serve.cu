@@ -192,7 +192,7 @@ extern "C" caat_status caat_sample_tokens(int64_t batch, int64_t vocab, caat_dty
                                           caat_stream_t stream)
 {
     if ((dt != CAAT_F32 && dt != CAAT_BF16) || batch < 0 || batch > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
-    if (vocab < 1 || vocab > 0x7fffffff - 65536 || ld < vocab || ld > ((int64_t)1 << 48)) return CAAT_ERR_INVALID_ARG;
+    if (vocab < 1 || vocab > (1 << 22) || ld < vocab || ld > ((int64_t)1 << 48)) return CAAT_ERR_INVALID_ARG;
     if (batch == 0) return CAAT_OK;
     for (const void *p : {logits, (const void *)u, (const void *)temperature, (const void *)top_k, (const void *)top_p,
                           (const void *)min_p, (const void *)token, (const void *)logprob})
