@@ -18,7 +18,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libcaat.so")
 
 SOURCES = ["api.cu", "select.cpp", "pcr.cu", "gemm_simt.cu", "gemm_tc.cu", "gemm_tc_bwd.cu", "decode.cu", "skinny_tc.cu", "noalloc.cu", "exchange.cu",
-           "serve.cu", "rope_append.cu", "paged_attn.cu", "sample.cu"]
+           "serve.cu", "rope_append.cu", "paged_attn.cu", "paged_attn_tc.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -76,6 +76,11 @@ __device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi)
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// many rows, bf16 (paged_attn_tc.cu)
+caat_status launch_paged_attention_tile(const PagedKV &kv, const PagedBatch &pb, int heads, const void *q, int64_t q_st,
+                                        int64_t q_sk, int64_t q_sg, float scale, int window, int sinks, void *o,
+                                        int64_t o_st, int64_t o_sh, cudaStream_t s);
+
 int *serve_error_word();             // device address of these kernels' error word, or null
 caat_status read_and_clear_serve_error();
 

@@ -544,6 +544,8 @@ caat_status launch_paged_attention(const PagedKV &kv, const PagedBatch &pb, int 
                  heads / kv.kv_heads, 1, serve_error_word(), kv, pb};
     if (p.err == nullptr) return CAAT_ERR_CUDA;
     const bool wide = (int64_t)pb.q_max * p.group > 8;
+    if (dt == CAAT_BF16 && (int64_t)pb.q_max * p.group > 64)
+        return launch_paged_attention_tile(kv, pb, heads, q, q_st, q_sk, q_sg, scale, window, sinks, o, o_st, o_sh, s);
     if (dt == CAAT_F32) {
         if (kv.dim <= 64) return launch_few<64, 1, true>(p, s);
         return launch_few<128, 1, true>(p, s);
