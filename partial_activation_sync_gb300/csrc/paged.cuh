@@ -5,7 +5,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "caat_internal.h"
 
@@ -63,17 +62,33 @@ __device__ __forceinline__ int64_t checked_page(int id, const PagedKV &kv, int *
     return -1;
 }
 
-// two e4m3 codes (low byte first) -> two f16, exact
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two)
+// Four e4m3 codes (low byte first) -> two pairs of f16, exact.  (The conversion
+// functions of cuda_fp8.h go through 16-bit halves: 3 to 4 more instructions a pair.)
+__device__ __forceinline__ void e4m3x4_f16(uint32_t four, uint32_t &lo, uint32_t &hi)
 {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
-// two floats -> two e4m3 codes, nearest even, magnitudes above 448 to 448, NaN kept
-__device__ __forceinline__ uint32_t f32x2_e4m3x2(float lo, float hi)
+// four floats -> four e4m3 codes, nearest even, magnitudes above 448 to 448, NaN kept
+__device__ __forceinline__ uint32_t f32x4_e4m3(float a, float b, float c, float d)
 {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// two floats -> two f16 in one register, nearest even
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // many rows, bf16 (paged_attn_tc.cu)

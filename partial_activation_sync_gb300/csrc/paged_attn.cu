@@ -66,12 +66,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // what pack_f16 rounded away
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed)
 {
@@ -79,18 +73,23 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
     return pack_f16(lo - f.x, hi - f.y);
 }
 
-template <int B>                     // B = 16 or 8 codes of one row, read once
+// B = 16 or 8 codes of one row, read once; zeros unless `live`.  Predicated, not
+// branched around: the loads of a group are then all in flight together.
+template <int B>
 __device__ __forceinline__ void load_codes(uint32_t (&w)[B / 4], const uint8_t *p, bool live)
 {
 #pragma unroll
     for (int i = 0; i < B / 4; ++i) w[i] = 0;
-    if (!live) return;
     if constexpr (B == 16) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "l"(p));
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                     "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3])
+                     : "l"(p), "r"((uint32_t)live));
     } else {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+                     "@q ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+                     : "+r"(w[0]), "+r"(w[1])
+                     : "l"(p), "r"((uint32_t)live));
     }
 }
 
@@ -264,8 +263,9 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
         for (int j = 0; j < G::NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint32_t a0 = e4m3x2_f16x2(x.k[0][j][e] & 0xffffu), a2 = e4m3x2_f16x2(x.k[0][j][e] >> 16);
-                const uint32_t a1 = e4m3x2_f16x2(x.k[1][j][e] & 0xffffu), a3 = e4m3x2_f16x2(x.k[1][j][e] >> 16);
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_f16(x.k[0][j][e], a0, a2);
+                e4m3x4_f16(x.k[1][j][e], a1, a3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     mma16816(s[t], a0, a1, a2, a3, qh[t][j][2 * e], qh[t][j][2 * e + 1]);
@@ -366,7 +366,9 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
                         float n[4] = {};
                         const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2, sh = 8 * (d & 3);
                         auto pair = [&](int u, int w) {
-                            return e4m3x2_f16x2(((bad[u][w] >> sh) & 0xffu) | (((bad[u + 1][w] >> sh) & 0xffu) << 8));
+                            uint32_t lo, hi;
+                            e4m3x4_f16(((bad[u][w] >> sh) & 0xffu) | (((bad[u + 1][w] >> sh) & 0xffu) << 8), lo, hi);
+                            return lo;
                         };
                         mma16816(n, pair(0, w0), pair(0, w1), pair(2, w0), pair(2, w1), b0, b1);
 #pragma unroll
@@ -383,10 +385,11 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
             const uint32_t pick = (d & 2) ? 0x7362u : 0x5140u;
             const uint32_t x0 = __byte_perm(x.v[0][w0], x.v[1][w0], pick), x1 = __byte_perm(x.v[0][w1], x.v[1][w1], pick);
             const uint32_t x2 = __byte_perm(x.v[2][w0], x.v[3][w0], pick), x3 = __byte_perm(x.v[2][w1], x.v[3][w1], pick);
-            const uint32_t a0 = e4m3x2_f16x2(x0 & 0xffffu), a1 = e4m3x2_f16x2(x1 & 0xffffu);
-            const uint32_t a2 = e4m3x2_f16x2(x2 & 0xffffu), a3 = e4m3x2_f16x2(x3 & 0xffffu);
-            const uint32_t e0 = e4m3x2_f16x2(x0 >> 16), e1 = e4m3x2_f16x2(x1 >> 16);
-            const uint32_t e2 = e4m3x2_f16x2(x2 >> 16), e3 = e4m3x2_f16x2(x3 >> 16);
+            uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
+            e4m3x4_f16(x0, a0, e0);
+            e4m3x4_f16(x1, a1, e1);
+            e4m3x4_f16(x2, a2, e2);
+            e4m3x4_f16(x3, a3, e3);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 mma16816(o[t][d], a0, a1, a2, a3, ph[t][0], ph[t][1]);

@@ -22,6 +22,8 @@
 //
 // When the blocks are fewer than the SMs, a cluster splits the keys of a row chunk and
 // joins its shares over distributed shared memory.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -32,9 +34,13 @@ using namespace tc;
 
 constexpr int TILE = 128;                    // rows of a tile; keys of a step
 constexpr int STAGES = 2;
-constexpr int WARPS = 17, THREADS = WARPS * 32;
-// warps 0-3 and 4-7: softmax of tile 0 and 1; 8-11: keys; 12-15: values; 16: products
-constexpr int W_KEYS = 8, W_VALUES = 12, W_MMA = 16;
+constexpr int WARPS = 28, THREADS = WARPS * 32;
+// warps 0-7 and 8-15: softmax of tile 0 and 1, two threads a row (64 columns each);
+// 16-19: keys to f16; 20-23: values to f16; 24: products (25 to 27 fill up the
+// warpgroup).  The block starts with 72 registers a thread, 896 * 72 = 64512; the
+// split gives out 512 * 80 + 256 * 72 + 128 * 40 = 64512 of them.
+constexpr int W_WIDEN = 16, W_VALUES = 20, W_MMA = 24;
+constexpr int REGS_SOFTMAX = 80, REGS_MMA = 40;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;
@@ -51,34 +57,38 @@ struct TileParams {
     PagedBatch pb;
 };
 
+struct Work {
+    int64_t t0;                              // first token's row
+    int b, h, pos0, row0, rows, p_lo, p_hi0, p_hi1, t_lo, n_sink, j_lo, steps, last0, last1;
+};
+
 struct Ctl {
-    uint64_t q_full[2], k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full[2], p_full[2];
+    Work work;
+    uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full[2], p_full[2];
     uint32_t tmem;
     int abort, v_nan;
     float ref_k, ref_v;
-    float part[2][4];
+    float part[2][8];
+    float up[2 * TILE], top[2][2][2 * TILE];     // [parity][half][row]
 };
 
 __host__ __device__ constexpr int half_bytes() { return TILE * 128; }       // 128 rows of 64 f16
 __host__ __device__ constexpr int tile_bytes(int DP) { return DP / 64 * half_bytes(); }
 __host__ __device__ constexpr int pitch(int DP) { return DP + 4; }          // floats of a row's share
+constexpr int CTL_BYTES = 6144;
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 __host__ __device__ constexpr int smem_bytes(int DP)
 {
     const int run = (2 + 2 * STAGES) * tile_bytes(DP);
     const int join = 2 * TILE * (pitch(DP) + 2) * 4;
-    return 1024 + 1024 + (run > join ? run : join);
+    return 1024 + CTL_BYTES + (run > join ? run : join);
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t f)
 {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 f)
-{
-    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), f);
-    return *reinterpret_cast<const uint32_t *>(&h);
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(f));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -86,6 +96,36 @@ __device__ __forceinline__ float exp2_approx(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction for two operations.
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]: A is 128 lanes of f16 pairs
@@ -105,7 +145,7 @@ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
     return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
                  "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -140,6 +180,58 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void bar_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// mbar_wait for warps that wait long beside busy ones: the thread sleeps in the wait (up
+// to 20 us at a time) instead of taking issue slots to ask again
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    uint64_t t0 = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        const uint64_t now = globaltimer();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > WAIT_NS) return false;
+    }
+}
+
+// barrier of `threads` threads that tells each whether any of them came with `flag`
+__device__ __forceinline__ bool bar_any(int id, int threads, bool flag)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(threads), "r"((uint32_t)flag)
+                 : "memory");
+    return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void give_up(volatile int *abort, int *err)
 {
     *abort = 1;
@@ -152,47 +244,57 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
     extern __shared__ uint8_t raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     Ctl *ctl = (Ctl *)base;
-    uint8_t *bufs = base + 1024;
+    uint8_t *bufs = base + CTL_BYTES;
     constexpr int TB = tile_bytes(DP), HB = half_bytes();
     const uint32_t q_s = smem_u32(bufs), k_s = q_s + 2 * TB, v_s = k_s + STAGES * TB;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort = &ctl->abort;
     const int P = p.kv.page, D = p.kv.dim;
 
-    const int split = (int)(blockIdx.x % p.splits);
-    int64_t unit = blockIdx.x / p.splits;
-    // the last rows of a prompt see the most keys: their chunks start first
-    const int64_t per_chunk = (int64_t)p.pb.batch * p.kv.kv_heads;
-    const int chunk = p.chunks - 1 - (int)(unit / per_chunk);
-    unit %= per_chunk;
-    const int h = (int)(unit % p.kv.kv_heads), b = (int)(unit / p.kv.kv_heads);
-    const Seq sq = load_seq(p.pb, P, b, p.err);
-    const int rows_all = sq.n * p.group;
-    const int row0 = chunk * 2 * TILE;
-    if (row0 >= rows_all) return;            // the whole cluster
-    const int rows = min(2 * TILE, rows_all - row0);
-    const int tiles = rows > TILE ? 2 : 1;
-    const int p_lo = sq.pos0 + row0 / p.group;
-    const int p_hi[2] = {sq.pos0 + (row0 + min(rows, TILE) - 1) / p.group, sq.pos0 + (row0 + rows - 1) / p.group};
-
-    // steps of 128 keys: those of the first tokens, then the window's
-    const int win_lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
-    const int t_lo = win_lo >> 7;
-    const int n_sink = min((int)(((int64_t)p.sinks + TILE - 1) >> 7), t_lo);
-    int nk[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) nk[t] = p_hi[t] < 0 ? 0 : n_sink + (p_hi[t] >> 7) + 1 - t_lo;
-    const int n_all = nk[tiles - 1];
-    const int j_lo = (int)((int64_t)n_all * split / p.splits), j_hi = (int)((int64_t)n_all * (split + 1) / p.splits);
-    const int steps = j_hi - j_lo;           // tile t takes part in the first `last[t]` of them
-    const int last[2] = {max(0, min(nk[0], j_hi) - j_lo), tiles > 1 ? steps : 0};
-    auto key0 = [&](int j) { return (j < n_sink ? j : t_lo + j - n_sink) << 7; };
+    // Which rows and keys are this block's: worked out by one thread, read from shared
+    // memory by each role as far as it needs them (registers are what the roles lack).
+    if (tid == 0) {
+        Work w;
+        const int split = (int)(blockIdx.x % p.splits);
+        int64_t unit = blockIdx.x / p.splits;
+        // the last rows of a prompt see the most keys: their chunks start first
+        const int64_t per_chunk = (int64_t)p.pb.batch * p.kv.kv_heads;
+        const int chunk = p.chunks - 1 - (int)(unit / per_chunk);
+        unit %= per_chunk;
+        w.h = (int)(unit % p.kv.kv_heads), w.b = (int)(unit / p.kv.kv_heads);
+        const Seq sq = load_seq(p.pb, P, w.b, p.err);
+        w.t0 = sq.t0, w.pos0 = sq.pos0;
+        w.row0 = chunk * 2 * TILE;
+        w.rows = min(2 * TILE, sq.n * p.group - w.row0);
+        if (w.rows > 0) {
+            w.p_lo = sq.pos0 + w.row0 / p.group;
+            w.p_hi0 = sq.pos0 + (w.row0 + min(w.rows, TILE) - 1) / p.group;
+            w.p_hi1 = sq.pos0 + (w.row0 + w.rows - 1) / p.group;
+            // steps of 128 keys: those of the first tokens, then the window's
+            const int win_lo = p.window > 0 ? max(0, w.p_lo - p.window + 1) : 0;
+            w.t_lo = win_lo >> 7;
+            w.n_sink = min((int)(((int64_t)p.sinks + TILE - 1) >> 7), w.t_lo);
+            const int nk0 = w.p_hi0 < 0 ? 0 : w.n_sink + (w.p_hi0 >> 7) + 1 - w.t_lo;
+            const int nk1 = w.p_hi1 < 0 ? 0 : w.n_sink + (w.p_hi1 >> 7) + 1 - w.t_lo;
+            w.j_lo = (int)((int64_t)nk1 * split / p.splits);
+            const int j_hi = (int)((int64_t)nk1 * (split + 1) / p.splits);
+            w.steps = j_hi - w.j_lo;         // a tile takes part in the first last0 / last1 of them
+            w.last0 = max(0, min(nk0, j_hi) - w.j_lo);
+            w.last1 = w.rows > TILE ? w.steps : 0;
+        }
+        ctl->work = w;
+    }
+    __syncthreads();
+    const Work &wk = ctl->work;
+    if (wk.rows <= 0) return;                // the whole cluster
+    auto last_of = [&](int t) { return t == 0 ? wk.last0 : wk.last1; };
+    const int key_sink = wk.n_sink, key_lo = wk.t_lo, j_lo = wk.j_lo, steps = wk.steps;
+    auto key0 = [&](int j) { return (j < key_sink ? j : key_lo + j - key_sink) << 7; };
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&ctl->q_full[i]), 4);
             mbar_init(smem_u32(&ctl->s_full[i]), 1);
-            mbar_init(smem_u32(&ctl->p_full[i]), 4);
+            mbar_init(smem_u32(&ctl->p_full[i]), 8);
         }
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&ctl->k_full[i]), 4);
@@ -208,113 +310,139 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
         tmem_alloc(smem_u32(&ctl->tmem), TMEM_COLS);
         tmem_relinquish();
     }
-    const int32_t *table = p.pb.table + (int64_t)b * p.pb.table_stride;
 
     // the largest scale of each side that the block's steps see
-    if (warp >= W_KEYS && warp < W_MMA && steps > 0) {
-        const bool keys = warp < W_VALUES;
-        const float *sc = keys ? p.kv.ks : p.kv.vs;
-        float m = 0.f;
+    if (warp >= W_WIDEN && warp < W_MMA && steps > 0) {
+        const int32_t *table = p.pb.table + (int64_t)wk.b * p.pb.table_stride;
+        const int h = wk.h, p_hi1 = wk.p_hi1;
+        float mk = 0.f, mv = 0.f;
         const int per = max(1, TILE >> p.kv.log2_page);          // pages of a step
         const int n = steps * per;
-        for (int i = tid & 127; i < n; i += 128) {
+        for (int i = tid & 255; i < n; i += 256) {
             const int key = key0(j_lo + i / per) + (i % per) * P;
-            if (key > p_hi[1]) continue;
+            if (key > p_hi1) continue;
             const int64_t pg = checked_page(__ldg(table + (key >> p.kv.log2_page)), p.kv, p.err);
-            if (pg >= 0) m = fmaxf(m, __ldg(sc + pg * p.kv.scale_stride + h));
+            if (pg >= 0) {
+                mk = fmaxf(mk, __ldg(p.kv.ks + pg * p.kv.scale_stride + h));
+                mv = fmaxf(mv, __ldg(p.kv.vs + pg * p.kv.scale_stride + h));
+            }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) ctl->part[keys ? 0 : 1][warp & 3] = m;
+        for (int o = 16; o > 0; o >>= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        }
+        if (lane == 0) ctl->part[0][warp & 7] = mk, ctl->part[1][warp & 7] = mv;
+    }
+    if (warp < W_WIDEN && last_of(warp >> 3) > 0) {
+        // Meanwhile the queries: rows as f16 times a power of two that brings a row's largest
+        // magnitude to [2^14, 2^15).  DP / 8 lanes load one row, 16 rows a warp; rows and
+        // dimensions beyond the last repeat it (unconditional loads, all in flight).
+        constexpr int LPR = DP / 8, RPW = 32 / LPR, N = 16 / RPW;    // lanes of a row, rows of a load, loads
+        const int t = warp >> 3, rq = (warp & 7) * 16 + lane / LPR, d = (lane % LPR) * 8;
+        const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + wk.t0 * p.q_st + wk.h * p.q_sk + min(d, D - 8);
+        const int row0 = wk.row0, n_rows = wk.rows;
+        uint4 w[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = row0 + min(t * TILE + rq + i * RPW, n_rows - 1);
+            w[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(at / p.group) * p.q_st + (int64_t)(at % p.group) * p.q_sg));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = fabsf(__uint_as_float(x[e] << 16)), z = fabsf(__uint_as_float(x[e] & 0xffff0000u));
+                m = fmaxf(m, fmaxf(a <= 3.402823466e38f ? a : 0.f, z <= 3.402823466e38f ? z : 0.f));
+            }
+            if (d >= D) m = 0.f;
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int e = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 127, -100) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            if (d == 0) ctl->up[t * TILE + rq + i * RPW] = up;
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[k] = pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
+            st_shared16(q_s + t * TB + (d >> 6) * HB + swizzled(rq + i * RPW, (d >> 3) & 7), y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tmem = ctl->tmem;
-    float ref[2];
+    auto ref_of = [&](int i) {
+        float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float m = fmaxf(fmaxf(ctl->part[i][0], ctl->part[i][1]), fmaxf(ctl->part[i][2], ctl->part[i][3]));
-        ref[i] = steps > 0 && m > 0.f ? m : 1.f;
-    }
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, ctl->part[i][k]);
+        return steps > 0 && m > 0.f ? m : 1.f;
+    };
+    // every row of a tile (positions from lo to hi) sees every key of the step from k0 on?
+    auto sees_all = [&](int k0, int lo, int hi) {
+        return k0 + TILE - 1 <= lo && (p.window == 0 || k0 > hi - p.window || k0 + TILE - 1 < p.sinks);
+    };
 
-    if (warp < W_KEYS) {
-        // ---------------- softmax: one thread a row
-        const int t = warp >> 2, r = tid & 127;
-        const int row = row0 + t * TILE + r;
-        const bool live = t * TILE + r < rows;
-        const int pos = sq.pos0 + row / p.group;
+    if (warp < W_WIDEN) {
+        // ---------------- softmax: two threads a row, 64 columns of S each; P over one's own
+        // columns, so that only the row's maximum is exchanged
+        more_registers<REGS_SOFTMAX>();
+        const int t = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, rt = t * TILE + r;
+        const int row = wk.row0 + rt, pos = wk.pos0 + row / p.group;
+        const bool live = rt < wk.rows;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_t = tmem + lanes + (uint32_t)t * TILE, o_t = tmem + lanes + O_COL + (uint32_t)t * TILE;
-        float c = 0.f, m_ref = -INFINITY, sum = 0.f;
+        const uint32_t s_t = tmem + lanes + (uint32_t)(t * TILE + 64 * hf), o_t = tmem + lanes + O_COL + (uint32_t)t * TILE;
+        const float c = p.scale_log2 / ctl->up[rt] * ref_of(0);
+        const int t_lo_pos = wk.pos0 + (wk.row0 + t * TILE) / p.group, t_hi_pos = t == 0 ? wk.p_hi0 : wk.p_hi1;
+        const int n_steps = last_of(t);
+        float m_ref = -INFINITY, sum = 0.f;
         bool ok = true;
-        if (last[t] > 0) {
-            // the row as f16 times a power of two that brings its largest magnitude to [2^14, 2^15)
-            const uint16_t *src = reinterpret_cast<const uint16_t *>(p.q) + (sq.t0 + row / p.group) * p.q_st +
-                                  h * p.q_sk + (row % p.group) * p.q_sg;
-            float m = 0.f;
-            for (int d = 0; d < D && live; d += 8) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + d));
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = fabsf(__uint_as_float(x[e] << 16)), z = fabsf(__uint_as_float(x[e] & 0xffff0000u));
-                    m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);
-                    m = fmaxf(m, z <= 3.402823466e38f ? z : 0.f);
-                }
-            }
-            const int e = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 127, -100) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            c = p.scale_log2 / up * ref[0];
-            for (int d = 0; d < D; d += 8) {
-                uint32_t y[4] = {0u, 0u, 0u, 0u};
-                if (live) {
-                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + d));
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        y[i] = pack_f16(__uint_as_float(x[i] << 16) * up, __uint_as_float(x[i] & 0xffff0000u) * up);
-                }
-                st_shared16(q_s + t * TB + (d >> 6) * HB + swizzled(r, (d >> 3) & 7), y[0], y[1], y[2], y[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->q_full[t]));
-        }
-        const int t_lo_pos = sq.pos0 + (row0 + t * TILE) / p.group, t_hi_pos = p_hi[t];
-        for (int j = 0; j < last[t]; ++j) {
-            ok = mbar_wait(smem_u32(&ctl->s_full[t]), (uint32_t)j & 1u, abort, WAIT_NS);
+        for (int j = 0; j < n_steps; ++j) {
+            ok = mbar_sleep(smem_u32(&ctl->s_full[t]), (uint32_t)j & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                give_up(abort, p.err);
-                break;
-            }
             fence_after_sync();
             const int k0 = key0(j_lo + j);
-            // every row of the tile sees every key of the step?
-            const bool all = k0 + TILE - 1 <= t_lo_pos &&
-                             (p.window == 0 || k0 > t_hi_pos - p.window || k0 + TILE - 1 < p.sinks);
-            // visible columns: [0, first) of the first tokens and (from, upto]
-            const int upto = pos - k0, from = p.window > 0 ? pos - p.window - k0 : -1;
-            const int first = p.window > 0 ? p.sinks - k0 : 0;
-            auto sees = [&](int col) { return col <= upto && (col > from || col < first); };
-            float mx = -INFINITY;
+            const bool all = sees_all(k0, t_lo_pos, t_hi_pos);
+            // the columns 32 q .. 32 q + 31 of this half that the row sees, as bits: up to its own
+            // position and within the window or among the first tokens
+            auto sees = [&](int q) {
+                const int at = k0 + 64 * hf + 32 * q;
+                auto bits_to = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };     // lowest n
+                return bits_to(pos - at + 1) &
+                       (p.window > 0 ? ~bits_to(pos - p.window - at + 1) | bits_to(p.sinks - at) : ~0u);
+            };
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (ok) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t v[32];
+                    tmem_ld32(s_t + 32 * q, v);
+                    if (all) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t v0[32], v1[32];
-                tmem_ld32x2(s_t + 64 * q, s_t + 64 * q + 32, v0, v1);
-                if (all) {
+                        for (int i = 0; i < 16; ++i)
+                            m4[i & 3] = max3(m4[i & 3], __uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    } else {
+                        const uint32_t seen = sees(q);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(v0[i]), __uint_as_float(v1[i])));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (sees(64 * q + i)) mx = fmaxf(mx, __uint_as_float(v0[i]));
-                        if (sees(64 * q + 32 + i)) mx = fmaxf(mx, __uint_as_float(v1[i]));
+                        for (int i = 0; i < 16; ++i)
+                            m4[i & 3] = max3(m4[i & 3], seen >> (2 * i) & 1 ? __uint_as_float(v[2 * i]) : -INFINITY,
+                                             seen >> (2 * i + 1) & 1 ? __uint_as_float(v[2 * i + 1]) : -INFINITY);
                     }
                 }
             }
-            mx *= c;
+            // the row's maximum of both halves (two buffers in turn: one barrier a step, which
+            // also makes the tile's warps give up together)
+            float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+            ctl->top[j & 1][hf][rt] = mx;
+            if (bar_any(1 + t, 256, !ok)) {
+                give_up(abort, p.err);
+                ok = false;
+                break;
+            }
+            mx = fmaxf(mx, ctl->top[j & 1][hf ^ 1][rt]) * c;
             const bool grow = mx > m_ref + LAZY;
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? exp2_approx(m_ref - mx) : 1.f;
@@ -322,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
                 sum *= f;
                 if (j > 0) {
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
+                    for (int d = 32 * hf; d < D; d += 64) {
                         uint32_t v[32];
                         tmem_ld32(o_t + d, v);
 #pragma unroll
@@ -332,26 +460,36 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
                 }
             }
             const float sub = m_ref == -INFINITY ? 0.f : m_ref;
-            float s0 = 0.f, s1 = 0.f;
+            uint64_t s2[2] = {0, 0};
+            const uint64_t c2 = pair_f32(c, c), sub2 = pair_f32(-sub, -sub);
+            // separate code for steps with a mask, so that the others have no branch among
+            // their exponentials
+            auto weights = [&](auto masked) {
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t v[32], w[16];
+                    tmem_ld32(s_t + 32 * q, v);
+                    const uint32_t seen = decltype(masked)::value ? sees(q) : ~0u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t v[32], w[16];
-                tmem_ld32(s_t + 32 * q, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a = fmaf(__uint_as_float(v[2 * i]), c, -sub), z = fmaf(__uint_as_float(v[2 * i + 1]), c, -sub);
-                    if (!all) {
-                        if (!sees(32 * q + 2 * i)) a = -INFINITY;
-                        if (!sees(32 * q + 2 * i + 1)) z = -INFINITY;
+                    for (int i = 0; i < 16; ++i) {
+                        float a, z;
+                        unpair(fma2(pair_f32(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), c2, sub2), a, z);
+                        if (decltype(masked)::value) {
+                            a = seen >> (2 * i) & 1 ? a : -INFINITY;
+                            z = seen >> (2 * i + 1) & 1 ? z : -INFINITY;
+                        }
+                        a = exp2_approx(a);
+                        z = exp2_approx(z);
+                        s2[i & 1] = add2(s2[i & 1], pair_f32(a, z));
+                        w[i] = pack_f16(a, z);
                     }
-                    a = exp2_approx(a);
-                    z = exp2_approx(z);
-                    s0 += a;
-                    s1 += z;
-                    w[i] = pack_f16(a, z);
+                    tmem_st16(s_t + 16 * q, w);
                 }
-                tmem_st16(s_t + 16 * q, w);
-            }
+            };
+            if (all) weights(std::false_type());
+            else weights(std::true_type());
+            float s0, s1;
+            unpair(add2(s2[0], s2[1]), s0, s1);
             sum += s0 + s1;
             tmem_wait_st();
             fence_before_sync();
@@ -359,213 +497,312 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
             if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[t]));
         }
         // the products' last commit follows the last step
-        if (ok && last[t] > 0) {
-            ok = mbar_wait(smem_u32(&ctl->s_full[t]), (uint32_t)last[t] & 1u, abort, WAIT_NS);
+        if (ok && n_steps > 0) {
+            ok = mbar_sleep(smem_u32(&ctl->s_full[t]), (uint32_t)n_steps & 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) give_up(abort, p.err);
             fence_after_sync();
         }
-        const bool have = ok && last[t] > 0;
+        ctl->top[0][hf][rt] = sum;
+        bar_sync(3, 512);                        // both tiles are done: the operands' memory is free
+        sum += ctl->top[0][hf ^ 1][rt];
+        if (*abort) ok = false;
+        const bool have = ok && n_steps > 0;
         const bool nan = have && *(volatile int *)&ctl->v_nan != 0;
+        const int h = wk.h;
+        // 32 columns of the accumulator from d on, NaN where a value the row sees is NaN
+        auto load_o = [&](int d, uint32_t (&v)[32]) {
+            if (have) {
+                tmem_ld32(o_t + d, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
+            if (nan && live) {
+                // rare: go through the codes of the row's keys
+                const int32_t *table = p.pb.table + (int64_t)wk.b * p.pb.table_stride;
+                for (int j = 0; j < n_steps; ++j)
+                    for (int i = 0; i < TILE; ++i) {
+                        const int key = key0(j_lo + j) + i;
+                        if (!(key <= pos && (p.window == 0 || key > pos - p.window || key < p.sinks))) continue;
+                        const int64_t pg = checked_page(__ldg(table + (key >> p.kv.log2_page)), p.kv, p.err);
+                        if (pg < 0) continue;
+                        const uint8_t *code = p.kv.v + pg * p.kv.page_stride + ((int64_t)h * P + (key & (P - 1))) * D;
+                        for (int e = 0; e < 32 && d + e < D; ++e)
+                            if ((code[d + e] & 0x7f) == 0x7f) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x)
+                                    if (x == e) v[x] = 0x7fffffffu;
+                            }
+                    }
+            }
+        };
+        auto out_row = [&](int at) {             // row of the output
+            return reinterpret_cast<__nv_bfloat16 *>(p.o) + (wk.t0 + at / p.group) * p.o_st +
+                   (int64_t)(h * p.group + at % p.group) * p.o_sh;
+        };
         if (p.splits == 1) {
-            if (ok && t < tiles) {
-                const float f = have && sum != 0.f ? ref[1] / sum : 0.f;
-                __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.o) + (sq.t0 + row / p.group) * p.o_st +
-                                     (h * p.group + row % p.group) * p.o_sh;
+            if (ok && t * TILE < wk.rows) {
+                // 32 columns at a time through this warp's 2 KB of shared memory, so that four
+                // lanes write 64 neighbouring bytes of a row
+                const float f = have && sum != 0.f ? ref_of(1) / sum : 0.f;
+                const uint32_t stage = q_s + (uint32_t)warp * 2048u;
 #pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
+                for (int d = 32 * hf; d < D; d += 64) {
                     uint32_t v[32];
-                    if (have) {
-                        tmem_ld32(o_t + d, v);
-                    } else {
+                    load_o(d, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    }
-                    if (nan) {
-                        // rare: a value the row sees is NaN; go through its keys' codes
-                        for (int j = 0; j < last[t] && live; ++j)
-                            for (int i = 0; i < TILE; ++i) {
-                                const int key = key0(j_lo + j) + i;
-                                if (!(key <= pos && (p.window == 0 || key > pos - p.window || key < p.sinks))) continue;
-                                const int64_t pg = checked_page(__ldg(table + (key >> p.kv.log2_page)), p.kv, p.err);
-                                if (pg < 0) continue;
-                                const uint8_t *code = p.kv.v + pg * p.kv.page_stride + ((int64_t)h * P + (key & (P - 1))) * D;
-                                for (int e = 0; e < 32 && d + e < D; ++e)
-                                    if ((code[d + e] & 0x7f) == 0x7f) {
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
 #pragma unroll
-                                        for (int x = 0; x < 32; ++x)
-                                            if (x == e) v[x] = 0x7fffffffu;
-                                    }
-                            }
-                    }
-                    if (live) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (d + 8 * i >= D) break;
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * e]) * f,
-                                                                               __uint_as_float(v[8 * i + 2 * e + 1]) * f);
-                                w[e] = *reinterpret_cast<const uint32_t *>(&x);
-                            }
-                            *reinterpret_cast<uint4 *>(out + d + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * e]) * f,
+                                                                           __uint_as_float(v[8 * i + 2 * e + 1]) * f);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&x);
                         }
+                        st_shared16(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), w[0], w[1], w[2], w[3]);
                     }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2), ch = lane & 3, at = wk.row0 + t * TILE + (warp & 3) * 32 + rr;
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(stage + rr * 64 + ((ch ^ (rr >> 1 & 3)) << 4)));
+                        if (at < wk.row0 + wk.rows && d + 8 * ch < D) *reinterpret_cast<uint4 *>(out_row(at) + d + 8 * ch) = x;
+                    }
+                    __syncwarp();
                 }
+            }
+        } else {
+            // this block's share of each row to its shared memory, then every block of the
+            // cluster joins some of the rows
+            constexpr int PITCH = pitch(DP);
+            float *share = reinterpret_cast<float *>(bufs), *stat = share + 2 * TILE * PITCH;     // stat: m, l of a row
+            const float f = ref_of(1);
+#pragma unroll 1
+            for (int d = 32 * hf; d < D; d += 64) {
+                uint32_t v[32];
+                load_o(d, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(share + rt * PITCH + d + 4 * i) =
+                        make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                    __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+            }
+            if (hf == 0) stat[2 * rt] = have ? m_ref : -INFINITY, stat[2 * rt + 1] = have ? sum : 0.f;
+            cluster_sync();
+            const uint32_t a_share = smem_u32(share), a_stat = smem_u32(stat);
+            const int per_row = D / 4, n = wk.rows * per_row;
+            for (int i = (int)cluster_ctarank() * 512 + tid; i < n; i += p.splits * 512) {
+                const int rr = i / per_row, d = 4 * (i % per_row);
+                float m = -INFINITY;
+                for (int k = 0; k < p.splits; ++k) m = fmaxf(m, ld_cluster(map_to_cta(a_stat + 8 * rr, (uint32_t)k)));
+                const float sub = m == -INFINITY ? 0.f : m;
+                float l = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < p.splits; ++k) {
+                    const float w = exp2_approx(ld_cluster(map_to_cta(a_stat + 8 * rr, (uint32_t)k)) - sub);
+                    const float4 x = ld_cluster4(map_to_cta(a_share + 4 * (rr * PITCH + d), (uint32_t)k));
+                    l += w * ld_cluster(map_to_cta(a_stat + 8 * rr + 4, (uint32_t)k));
+                    o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+                }
+                const float g = l != 0.f ? 1.f / l : 0.f;
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * g, o.y * g), hi = __floats2bfloat162_rn(o.z * g, o.w * g);
+                *reinterpret_cast<uint2 *>(out_row(wk.row0 + rr) + d) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             }
         }
     } else if (warp < W_MMA) {
-        // ---------------- codes to f16: keys (warps 8-11) and values (12-15)
-        const bool keys = warp < W_VALUES;
-        constexpr int CH = DP / 16;              // 16-code chunks of a row: lanes of a row
-        constexpr int RPL = 32 / CH;             // rows of one load of the warp
-        constexpr int LOADS = 32 / RPL;          // loads for the warp's 32 rows
-        const int ch = lane % CH, rl = lane / CH;
+        // ---------------- codes to f16: a warp widens 32 keys, or values, of a step
+        // A load of the warp covers RPL rows: four lanes for the 64 codes of one row's half, so
+        // that the eight lanes of a 128-byte store meet rows of both parities and with them,
+        // through the swizzle, all banks.
+        constexpr int HALVES = DP / 64, RPL = 8 / HALVES, LOADS = 32 / RPL;
+        const int half = HALVES == 2 ? lane >> 4 : 0, rl = (lane >> 2) & (RPL - 1), ch = 4 * half + (lane & 3);
         const int r_base = (warp & 3) * 32;
-        const uint8_t *codes = (keys ? p.kv.k : p.kv.v) + (int64_t)h * P * D;
-        const float *sc = keys ? p.kv.ks : p.kv.vs;
-        const float r_ref = 1.f / ref[keys ? 0 : 1];
-        const uint32_t stage0 = keys ? k_s : v_s;
-        uint64_t *full = keys ? ctl->k_full : ctl->v_full, *empty = keys ? ctl->k_empty : ctl->v_empty;
-        const bool in = ch * 16 < D;
-        // the warp's rows are two groups of 16 keys, each within a page
+        const bool keys = warp < W_VALUES, in = ch * 16 < D;
+        const int h = wk.h, p_hi1 = wk.p_hi1;
+        const int32_t *table = p.pb.table + (int64_t)wk.b * p.pb.table_stride;
+        const uint8_t *codes = (keys ? p.kv.k : p.kv.v) + (int64_t)h * P * D + rl * D + (in ? ch * 16 : 0);
+        const float *scales = (keys ? p.kv.ks : p.kv.vs) + h;
+        const float r_ref = 1.f / ref_of(keys ? 0 : 1);
+        const uint32_t full = smem_u32(keys ? ctl->k_full : ctl->v_full), empty = smem_u32(keys ? ctl->k_empty : ctl->v_empty);
+        // the first chunk of row r_base + i * RPL + rl; the second is 16 bytes across (xor)
+        uint32_t to[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            to[i] = (keys ? k_s : v_s) + half * HB + swizzled(r_base + (HALVES == 2 ? 4 * i : 8 * i) + rl, 2 * (lane & 3));
+        // the warp's rows are two groups of 16 keys, each within a page; groups beyond the
+        // last visible key read page 0 and count with scale 0
+        auto group_key = [&](int j, int g) { return key0(j_lo + j) + r_base + 16 * g; };
         auto page_id = [&](int j, int g) {
-            const int key = key0(j_lo + j) + r_base + 16 * g;
-            return j < steps && key <= p_hi[1] ? __ldg(table + (key >> p.kv.log2_page)) : -1;
+            const int key = group_key(j, g);
+            return j < steps && key <= p_hi1 ? __ldg(table + (key >> p.kv.log2_page)) : 0;
         };
         uint4 cur[LOADS];
-        float f_cur[2];
-        auto load = [&](int j, const int (&id)[2]) {
+        float sc[2];
+        auto load = [&](int j, int id0, int id1) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int key = key0(j_lo + j) + r_base + 16 * g;
-                int64_t pg = -1;
-                if (id[g] >= 0 || (j < steps && key <= p_hi[1])) pg = checked_page(id[g], p.kv, p.err);
-                f_cur[g] = pg >= 0 ? __ldg(sc + pg * p.kv.scale_stride + h) * r_ref : 0.f;
-                const uint8_t *src = codes + (pg >= 0 ? pg : 0) * p.kv.page_stride + (int64_t)(key & (P - 1)) * D + ch * 16;
+                const int64_t pg = max((int64_t)0, checked_page(g == 0 ? id0 : id1, p.kv, p.err));
+                sc[g] = __ldg(scales + pg * p.kv.scale_stride);
+                const uint8_t *src = codes + pg * p.kv.page_stride + (group_key(j, g) & (P - 1)) * D;
 #pragma unroll
-                for (int i = 0; i < LOADS / 2; ++i) {
-                    const int r = i * RPL + rl;
-                    cur[g * (LOADS / 2) + i] =
-                        pg >= 0 && in ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)r * D)) : make_uint4(0, 0, 0, 0);
-                }
+                for (int i = 0; i < LOADS / 2; ++i)
+                    cur[g * (LOADS / 2) + i] = __ldg(reinterpret_cast<const uint4 *>(src + i * (RPL * D)));
             }
         };
-        int id[2] = {page_id(0, 0), page_id(0, 1)};
-        if (steps > 0) load(0, id);
-        id[0] = page_id(1, 0);
-        id[1] = page_id(1, 1);
+        if (steps > 0) load(0, page_id(0, 0), page_id(0, 1));
         bool ok = true;
-        uint32_t bad = 0;
         for (int j = 0; j < steps; ++j) {
             const int st = j % STAGES;
-            ok = mbar_wait(smem_u32(&empty[st]), ((uint32_t)(j / STAGES) & 1u) ^ 1u, abort, WAIT_NS);
+            const int id0 = page_id(j + 1, 0), id1 = page_id(j + 1, 1);      // used after this step's work
+            ok = mbar_sleep(empty + 8 * st, ((uint32_t)(j / STAGES) & 1u) ^ 1u, abort);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                give_up(abort, p.err);
-                break;
-            }
-            const uint32_t dst = stage0 + st * TB + (ch >> 2) * HB;
-            const int k0 = key0(j_lo + j);
+            if (!ok) break;
+            // In a step that some row does not see in full, its weight 0 times a NaN value would
+            // be NaN: look for NaN codes (0x7f + 1 carries into the sign bit of the masked byte)
+            // and, rarely, take them out of what this lane stores below.  Where some row may see
+            // one, the epilogue looks for it.
+            bool nan = false;
+            if (!keys && !sees_all(key0(j_lo + j), wk.p_lo, p_hi1)) {
+                uint32_t any = 0;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int g = i / (LOADS / 2);
-                const int r = r_base + i * RPL + rl;
-                uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-                if (!keys) {
-                    // NaN values are taken out; where some row may see one, the epilogue looks
-                    // for it (0x7f + 1 and 0xff + 1 carry into the sign bit of the masked byte)
-                    uint32_t nan[4], any = 0;
+                for (int i = 0; i < LOADS; ++i)
+                    any |= ((cur[i].x & 0x7f7f7f7fu) + 0x01010101u) | ((cur[i].y & 0x7f7f7f7fu) + 0x01010101u) |
+                           ((cur[i].z & 0x7f7f7f7fu) + 0x01010101u) | ((cur[i].w & 0x7f7f7f7fu) + 0x01010101u);
+                nan = in && (any & 0x80808080u);
+            }
+            if (in) {
+                const float a0 = group_key(j, 0) <= p_hi1 ? sc[0] * r_ref : 0.f, a1 = group_key(j, 1) <= p_hi1 ? sc[1] * r_ref : 0.f;
+                const uint32_t f0 = pack_f16(a0, a0), f1 = pack_f16(a1, a1);
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) {
+                    const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w}, f = i < LOADS / 2 ? f0 : f1;
+                    uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        nan[e] = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        any |= nan[e];
+                        e4m3x4_f16(w[e], y[2 * e], y[2 * e + 1]);
+                        y[2 * e] = mul_f16x2(y[2 * e], f);
+                        y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
                     }
-                    if (any) {
-                        if (k0 + r <= p_hi[1]) bad = 1;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] &= ~((nan[e] >> 7) * 0xffu);
-                    }
-                }
-                const __half2 f = __float2half2_rn(f_cur[g]);
-                uint32_t y[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[2 * e] = mul_f16x2(e4m3x2_f16x2(w[e] & 0xffffu), f);
-                    y[2 * e + 1] = mul_f16x2(e4m3x2_f16x2(w[e] >> 16), f);
-                }
-                // lanes of the two 64-column halves store their two chunks in opposite order,
-                // so that eight lanes always meet eight different bank groups
-                const int flip = (ch >> 2) & 1, c2 = (ch & 3) * 2;
-                if (in) {
-                    const uint32_t a0 = dst + swizzled(r, c2 + flip), a1 = dst + swizzled(r, c2 + 1 - flip);
-                    st_shared16(a0, flip ? y[4] : y[0], flip ? y[5] : y[1], flip ? y[6] : y[2], flip ? y[7] : y[3]);
-                    st_shared16(a1, flip ? y[0] : y[4], flip ? y[1] : y[5], flip ? y[2] : y[6], flip ? y[3] : y[7]);
+                    const uint32_t at = to[i & 1] + (uint32_t)(st * TB) + (i >> 1) * (HALVES == 2 ? 1024u : 2048u);
+                    st_shared16(at, y[0], y[1], y[2], y[3]);
+                    st_shared16(at ^ 16u, y[4], y[5], y[6], y[7]);
                 }
             }
-            if (bad) *(volatile int *)&ctl->v_nan = 1;
+            if (nan) {
+                const int k0 = key0(j_lo + j);
+#pragma unroll 1
+                for (int i = 0; i < 2 * LOADS; ++i) {
+                    const int r = r_base + (i >> 1) * RPL + rl;
+                    const uint32_t at = v_s + st * TB + half * HB + swizzled(r, 2 * (lane & 3) + (i & 1));
+                    uint32_t w[4], gone = 0;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(at));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t nan = ((w[e] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+                        gone |= nan;
+                        w[e] &= ~((nan >> 15) * 0xffffu);
+                    }
+                    if (gone) {
+                        st_shared16(at, w[0], w[1], w[2], w[3]);
+                        if (k0 + r <= p_hi1) *(volatile int *)&ctl->v_nan = 1;
+                    }
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[st]));
-            if (j + 1 < steps) load(j + 1, id);
-            id[0] = page_id(j + 2, 0);
-            id[1] = page_id(j + 2, 1);
+            if (lane == 0) mbar_arrive(full + 8 * st);
+            if (j + 1 < steps) load(j + 1, id0, id1);
         }
+        if (!ok) give_up(abort, p.err);
     } else {
-        // ---------------- products, issued by one thread
-        if (lane == 0) {
-            const uint32_t id_s = idesc_f16(TILE, TILE, false), id_o = idesc_f16(TILE, D, true);
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t ph) {
-                ok = ok && mbar_wait(smem_u32(bar), ph & 1u, abort, WAIT_NS);
-                fence_after_sync();
-            };
-            auto scores = [&](int t, int j) {
-                const uint32_t a = q_s + t * TB, bk = k_s + (j % STAGES) * TB;
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * HB + (uint32_t)(k & 3) * 32u;
-                    mma_f16(tmem + t * TILE, desc_kmajor_sw128(a + off), desc_kmajor_sw128(bk + off), id_s, k > 0);
-                }
-                mma_commit(smem_u32(&ctl->s_full[t]));
-            };
-            auto outputs = [&](int t, int j) {
-                const uint32_t bv = v_s + (j % STAGES) * TB;
+        fewer_registers<REGS_MMA>();
+        // ---------------- products, of tile 0 and tile 1 in turn: the tiles then stay half a
+        // step apart, one's softmax beside the other's products.  The whole warp keeps the
+        // pace, one lane issues (code that only one lane runs would compute each descriptor
+        // in vector registers and move it: 107 cycles a product instead of the 64 it takes).
+        const int mine = warp == W_MMA ? steps : 0, last0 = wk.last0, last1 = wk.last1;
+        const uint32_t id_s = idesc_f16(TILE, TILE, false), id_o = idesc_f16(TILE, D, true);
+        const bool one = elect_one();
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t ph) {
+            ok = ok && mbar_sleep(smem_u32(bar), ph & 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (one) mma_commit(smem_u32(bar));
+        };
+        // descriptors differ in their start address (16-byte units, low bits) alone
+        const uint64_t dq = desc_kmajor_sw128(q_s), dk = desc_kmajor_sw128(k_s), dv = desc_sw128(v_s, HB, 1024u);
+        auto scores = [&](int t, uint32_t st) {
+            const uint64_t a = dq + (uint32_t)(t * (TB >> 4)), bk = dk + st * (uint32_t)(TB >> 4);
+            const uint32_t s_t = tmem + t * TILE;
+            if (D == DP) {
+                if (one)
 #pragma unroll
-                for (int k = 0; k < TILE / 16; ++k)
-                    mma_f16_ta(tmem + O_COL + t * TILE, tmem + t * TILE + 8 * k, desc_sw128(bv + 2048u * k, HB, 1024u), id_o,
-                               j > 0 || k > 0);
-            };
-            for (int t = 0; t < tiles; ++t)
-                if (last[t] > 0) wait(&ctl->q_full[t], 0);
-            if (steps > 0) {
-                wait(&ctl->k_full[0], 0);
-                if (ok) {
-                    for (int t = 0; t < 2; ++t)
-                        if (last[t] > 0) scores(t, 0);
-                    mma_commit(smem_u32(&ctl->k_empty[0]));
-                }
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_f16(s_t, a + (uint32_t)((k >> 2) * (HB >> 4) + (k & 3) * 2),
+                                bk + (uint32_t)((k >> 2) * (HB >> 4) + (k & 3) * 2), id_s, k > 0);
+            } else {
+                if (one)
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (uint32_t)((k >> 2) * (HB >> 4) + (k & 3) * 2);
+                        mma_f16(s_t, a + off, bk + off, id_s, k > 0);
+                    }
             }
-            for (int j = 0; j < steps && ok; ++j) {
-                const uint32_t ph = (uint32_t)(j / STAGES), st = j % STAGES;
-                wait(&ctl->v_full[st], ph);
-                if (j + 1 < steps) wait(&ctl->k_full[(j + 1) % STAGES], (uint32_t)((j + 1) / STAGES));
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= last[t]) continue;
-                    wait(&ctl->p_full[t], (uint32_t)j);
-                    if (!ok) break;
-                    outputs(t, j);
-                    if (j + 1 < last[t]) scores(t, j + 1);
-                    else mma_commit(smem_u32(&ctl->s_full[t]));
-                }
-                if (ok) {
-                    mma_commit(smem_u32(&ctl->v_empty[st]));
-                    if (j + 1 < steps) mma_commit(smem_u32(&ctl->k_empty[(j + 1) % STAGES]));
-                }
+        };
+        auto outputs = [&](int t, uint32_t st, uint32_t acc) {
+            const uint64_t bv = dv + st * (uint32_t)(TB >> 4);
+            const uint32_t s_t = tmem + t * TILE, o_t = tmem + O_COL + t * TILE;
+            if (one) {
+                mma_f16_ta(o_t, s_t, bv, id_o, acc);
+#pragma unroll
+                for (int k = 1; k < TILE / 16; ++k)
+                    mma_f16_ta(o_t, s_t + 8 * k + (k >= 4 ? 32 : 0), bv + 128u * k, id_o, 1u);
             }
-            if (!ok) give_up(abort, p.err);
+        };
+        if (mine > 0) {
+            wait(&ctl->k_full[0], 0);
+            fence_after_sync();
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (ok && (t == 0 ? last0 : last1) > 0) {
+                    scores(t, 0);
+                    commit(&ctl->s_full[t]);
+                }
+            if (ok) commit(&ctl->k_empty[0]);
         }
-        __syncwarp();
+        for (int j = 0; j < mine && ok; ++j) {
+            const uint32_t st = (uint32_t)j % STAGES, next = (uint32_t)(j + 1) % STAGES;
+            wait(&ctl->v_full[st], (uint32_t)(j / STAGES));
+            if (j + 1 < mine) wait(&ctl->k_full[next], (uint32_t)((j + 1) / STAGES));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int last = t == 0 ? last0 : last1;
+                if (j >= last || !ok) continue;
+                wait(&ctl->p_full[t], (uint32_t)j);
+                fence_after_sync();
+                if (!ok) continue;
+                outputs(t, st, j > 0);
+                if (j + 1 < last) scores(t, next);
+                commit(&ctl->s_full[t]);
+            }
+            if (ok) {
+                commit(&ctl->v_empty[st]);
+                if (j + 1 < mine) commit(&ctl->k_empty[next]);
+            }
+        }
+        if (!ok) give_up(abort, p.err);
+    }
+    if (p.splits > 1) {
+        if (warp >= W_WIDEN) cluster_sync();     // the softmax warps came by between share and join
+        cluster_sync();                          // no block leaves while another reads its shares
     }
     fence_before_sync();
     __syncthreads();
@@ -590,12 +827,26 @@ caat_status launch_tile(TileParams &p, cudaStream_t s)
     const int64_t units = (int64_t)p.pb.batch * p.kv.kv_heads * chunks;
     if (chunks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     p.chunks = (int)chunks;
+    // fewer blocks than SMs: clusters share the keys of a chunk, at least four steps each
+    int64_t keys = (int64_t)p.pb.width * p.kv.page;
+    if (p.window > 0 && keys > (int64_t)p.window + p.sinks + p.pb.q_max) keys = (int64_t)p.window + p.sinks + p.pb.q_max;
     p.splits = 1;
+    while (p.splits < 8 && 2 * units * p.splits <= num_sms() && keys >= (int64_t)p.splits * 8 * TILE) p.splits *= 2;
     if (units * p.splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     auto kern = paged_attn_tile_kernel<DP>;
     if (prepare_kernel_smem((const void *)kern, smem_bytes(DP)) != CAAT_OK) return CAAT_ERR_CUDA;
-    kern<<<(unsigned)(units * p.splits), THREADS, smem_bytes(DP), s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(units * p.splits));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes(DP);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("paged_attn_tile");
     return CAAT_OK;
 }

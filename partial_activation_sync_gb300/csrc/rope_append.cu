@@ -124,14 +124,11 @@ __device__ void rescale_rows(uint8_t *codes, int bytes, float ratio, int me, int
         uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t r = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t f = e4m3x2_f16x2((x[j] >> (16 * h)) & 0xffffu);
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&f));
-                r |= f32x2_e4m3x2(v.x * ratio, v.y * ratio) << (16 * h);
-            }
-            x[j] = r;
+            uint32_t lo, hi;
+            e4m3x4_f16(x[j], lo, hi);
+            const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            x[j] = f32x4_e4m3(u.x * ratio, u.y * ratio, v.x * ratio, v.y * ratio);
         }
         *reinterpret_cast<uint4 *>(codes + i) = make_uint4(x[0], x[1], x[2], x[3]);
     }
@@ -142,8 +139,7 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int d0, int d1, const 
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = f32x2_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-               (f32x2_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+        w[i] = f32x4_e4m3(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
     *reinterpret_cast<uint2 *>(row + d0) = make_uint2(w[0], w[1]);
     *reinterpret_cast<uint2 *>(row + d1) = make_uint2(w[2], w[3]);
 }

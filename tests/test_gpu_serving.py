@@ -111,6 +111,10 @@ def test_attention_long_split_over_blocks():
     # one sequence over many blocks of a cluster, with an odd tail
     _attention([1], [5003], 4, 1, 128, 64, "bf16", seed=5)
     _attention([1], [5003], 2, 2, 48, 16, "f32", seed=6)
+    # many rows of few heads: the tile kernel's split, whole, with a window, and ragged
+    _attention([150], [3000], 4, 2, 128, 64, "bf16", seed=7)
+    _attention([150], [3000], 4, 2, 64, 16, "bf16", window=1500, sinks=200, seed=8)
+    _attention([70, 3, 200], [2500, 40, 200], 2, 1, 96, 32, "bf16", seed=9)
 
 
 def test_attention_rows_that_see_nothing_are_zero():
