@@ -34,13 +34,12 @@ using namespace tc;
 
 constexpr int TILE = 128;                    // rows of a tile; keys of a step
 constexpr int STAGES = 2;
-constexpr int WARPS = 28, THREADS = WARPS * 32;
+constexpr int WARPS = 26, THREADS = WARPS * 32;
 // warps 0-7 and 8-15: softmax of tile 0 and 1, two threads a row (64 columns each);
-// 16-19: keys to f16; 20-23: values to f16; 24: products (25 to 27 fill up the
-// warpgroup).  The block starts with 72 registers a thread, 896 * 72 = 64512; the
-// split gives out 512 * 80 + 256 * 72 + 128 * 40 = 64512 of them.
+// 16-19: keys to f16; 20-23: values to f16; 24: products.  A 26th warp idles: with it the
+// compiler lays the products' loop out so that a 4096-token prompt (32 heads of 128) takes
+// 161 us, without it 174.
 constexpr int W_WIDEN = 16, W_VALUES = 20, W_MMA = 24;
-constexpr int REGS_SOFTMAX = 80, REGS_MMA = 40;
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;
@@ -185,12 +184,12 @@ __device__ __forceinline__ void bar_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// mbar_wait for warps that wait long beside busy ones: the thread sleeps in the wait (up
-// to 20 us at a time) instead of taking issue slots to ask again
+// mbar_wait for warps that wait beside busy ones: a hint to sleep in the wait, and the clock
+// and the abort flag looked at once in 64 rounds, so that waiting takes few issue slots
 __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volatile int *abort)
 {
     uint64_t t0 = 0;
-    while (true) {
+    for (int i = 0;; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -200,6 +199,7 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, volati
             : "r"(bar), "r"(parity), "r"(20000u)
             : "memory");
         if (ok) return true;
+        if (i & 63) continue;
         if (*abort) return false;
         const uint64_t now = globaltimer();
         if (t0 == 0) t0 = now;
@@ -218,11 +218,6 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool flag)
                  : "memory");
     return r != 0;
 }
-
-template <int N>
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one()
@@ -389,7 +384,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
     if (warp < W_WIDEN) {
         // ---------------- softmax: two threads a row, 64 columns of S each; P over one's own
         // columns, so that only the row's maximum is exchanged
-        more_registers<REGS_SOFTMAX>();
         const int t = warp >> 3, hf = (warp >> 2) & 1, r = (warp & 3) * 32 + lane, rt = t * TILE + r;
         const int row = wk.row0 + rt, pos = wk.pos0 + row / p.group;
         const bool live = rt < wk.rows;
@@ -722,7 +716,6 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
         }
         if (!ok) give_up(abort, p.err);
     } else {
-        fewer_registers<REGS_MMA>();
         // ---------------- products, of tile 0 and tile 1 in turn: the tiles then stay half a
         // step apart, one's softmax beside the other's products.  The whole warp keeps the
         // pace, one lane issues (code that only one lane runs would compute each descriptor
