@@ -469,8 +469,8 @@ caat_status caat_rank_fold(int t, int64_t rows, int64_t cols, caat_dtype dt, con
  *
  * The cache of one layer holds pages of `page` tokens (16, 32, 64 or 128).  k and v
  * are e4m3 codes [pages, kv_heads, page, dim], the last three dimensions dense and
- * pages page_stride elements apart; k_scale and v_scale are fp32 [pages, kv_heads],
- * rows scale_stride apart.  A cached value is code * scale; scales are positive
+ * pages page_stride elements apart (below 2^32); k_scale and v_scale are fp32 [pages,
+ * kv_heads], rows scale_stride apart.  A cached value is code * scale; scales are positive
  * powers of two.  dim is a multiple of 16 up to 128; codes are 16-byte aligned.
  */
 typedef struct {

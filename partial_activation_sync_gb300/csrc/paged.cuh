@@ -96,6 +96,11 @@ caat_status launch_paged_attention_tile(const PagedKV &kv, const PagedBatch &pb,
                                         int64_t q_sk, int64_t q_sg, float scale, int window, int sinks, void *o,
                                         int64_t o_st, int64_t o_sh, cudaStream_t s);
 
+// Launch attributes of these kernels: a cluster of `cluster` blocks (1: none), and a
+// programmatic dependent of the previous launch unless CAAT_PDL=0 (the kernel waits for
+// that launch before its first access).  Returns how many attributes it set.
+unsigned serve_attrs(cudaLaunchAttribute (&attr)[2], int cluster);
+
 int *serve_error_word();             // device address of these kernels' error word, or null
 caat_status read_and_clear_serve_error();
 

@@ -19,7 +19,7 @@
 // latter become pairs along the keys by byte permutes.
 //
 // Codes become f16, which holds every e4m3 value.  Queries become f16 times a power
-// of two for each row, and weights f16 times 2^8: 11 bits against the 8 of bf16, at
+// of two for each row, and weights f16 times 2^4: 11 bits against the 8 of bf16, at
 // the same speed.  fp32 queries are split into two f16 (22 bits), as are the weights,
 // at twice the products.  The scales of a page multiply the scores after the product
 // (keys) and the weights before it (values), in fp32.
@@ -34,7 +34,8 @@ using tc::map_to_cta;
 using tc::smem_u32;
 
 constexpr int WARPS = 4;
-constexpr float P_BIAS = 8.f;        // weights are held times 2^8
+constexpr float P_BIAS = 4.f;        // weights are held times 2^4 ...
+constexpr float LAZY = 8.f;          // ... of a maximum that may lag by 2^8: 2^12 at most in f16
 
 struct AttnParams {
     const void *q;
@@ -111,25 +112,28 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 // DP: head dimension rounded up to 64 or 128.  NT: row tiles of 8.  F32: fp32
-// queries and output (both operands of the products in two f16 parts).
+// queries and output (both operands of the products in two f16 parts).  A step of a warp
+// is 4 KB of cache: KG groups of 16 keys.
 template <int DP, int NT, bool F32>
 struct Geo {
     static constexpr int NJ = DP / 64;           // 16-code loads of a key for each lane
     static constexpr int VB = DP / 8;            // value codes of one key for each lane
+    static constexpr int KG = 128 / DP, KEYS = 16 * KG, LOG_KEYS = KG == 2 ? 5 : 4;
     static constexpr int ROWS = 8 * NT;
     static constexpr int PART = DP + 4;          // floats of one row's share: o, m, l, pad
+    static constexpr int MIN_BLOCKS = F32 ? 2 : NT == 2 ? (DP == 64 ? 3 : 2) : (DP == 64 ? 4 : 3);
 };
 
-// The codes of one group of 16 keys, as one lane holds them.
+// The codes of one step, as one lane holds them.
 template <int DP>
 struct Codes {
-    uint32_t k[2][DP / 64][4];                   // keys r and r + 8
-    uint32_t v[4][DP / 32];                      // keys 2c, 2c + 1, 2c + 8, 2c + 9
-    float ks, vs;
+    uint32_t k[128 / DP][2][DP / 64][4];         // of each group: keys r and r + 8
+    uint32_t v[128 / DP][4][DP / 32];            // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    float ks[128 / DP], vs[128 / DP];
 };
 
 template <int DP, int NT, bool F32>
-__global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_attn_few_kernel(AttnParams p, int splits)
+__global__ void __launch_bounds__(WARPS * 32, Geo<DP, NT, F32>::MIN_BLOCKS) paged_attn_few_kernel(AttnParams p, int splits)
 {
     using G = Geo<DP, NT, F32>;
     extern __shared__ float sm[];                // [WARPS + 1][ROWS][PART]
@@ -142,6 +146,9 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
     const int h = (int)(unit % p.kv.kv_heads), b = (int)(unit / p.kv.kv_heads);
     const int P = p.kv.page, D = p.kv.dim;
 
+    // a programmatic dependent of the previous launch: wait for it before the first access
+    tc::griddep_wait();
+    tc::griddep_launch_dependents();
     const Seq sq = load_seq(p.pb, P, b, p.err);
     const int rows_all = sq.n * p.group;
     const int row0 = chunk * G::ROWS;
@@ -149,11 +156,72 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
     const int rows = min(G::ROWS, rows_all - row0);
     const int p_lo = sq.pos0 + row0 / p.group, p_hi = sq.pos0 + (row0 + rows - 1) / p.group;
 
-    // groups of 16 keys that some row sees: those of the first tokens, then the window's
+    // steps that some row sees something of: those of the first tokens, then the window's
     const int win_lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
-    const int g_lo = win_lo >> 4;
-    const int n_sink = min((p.sinks + 15) >> 4, g_lo);
-    const int n_grp = p_hi < 0 ? 0 : n_sink + ((p_hi >> 4) + 1 - g_lo);
+    const int g_lo = win_lo >> G::LOG_KEYS;
+    const int n_sink = min((p.sinks + G::KEYS - 1) >> G::LOG_KEYS, g_lo);
+    const int n_grp = p_hi < 0 ? 0 : n_sink + ((p_hi >> G::LOG_KEYS) + 1 - g_lo);
+
+    float o[NT][G::VB / 2][4], mx[NT][2], sum[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int i = 0; i < G::VB / 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+        mx[t][0] = mx[t][1] = -INFINITY;
+        sum[t][0] = sum[t][1] = 0.f;
+    }
+    float ref = 0.f, inv_ref = 0.f;              // o counts in units of this value scale
+
+    const int32_t *table = p.pb.table + (int64_t)b * p.pb.table_stride;
+    const int64_t head = (int64_t)h * P * D;
+    const uint8_t *kbase = p.kv.k + head + r * D + c * 16, *vbase = p.kv.v + head + 2 * c * D + r * G::VB;
+    const uint32_t page_stride = (uint32_t)p.kv.page_stride, scale_stride = (uint32_t)p.kv.scale_stride;
+    auto key_of = [&](int i) { return (i < n_sink ? i : g_lo + i - n_sink) << G::LOG_KEYS; };
+    // pages of a step's groups (16 keys lie within a page)
+    auto pages_of = [&](int i, int (&id)[G::KG]) {
+#pragma unroll
+        for (int g = 0; g < G::KG; ++g) {
+            const int key = key_of(i) + 16 * g;
+            id[g] = i < n_grp && key <= p_hi ? __ldg(table + (key >> p.kv.log2_page)) : 0;
+        }
+    };
+    auto load = [&](Codes<DP> &x, int i, const int (&id)[G::KG]) {
+#pragma unroll
+        for (int g = 0; g < G::KG; ++g) {
+            const int key = key_of(i) + 16 * g;
+            bool live = i < n_grp && key <= p_hi;
+            uint32_t pg = (uint32_t)id[g];
+            if (pg >= (uint32_t)p.kv.pages) {    // no such page: nothing is read for it
+                if (live) *(volatile int *)p.err = CAAT_ERR_INVALID_ARG;
+                live = false;
+                pg = 0;
+            }
+            const uint64_t at = (uint64_t)pg * page_stride + (uint32_t)((key & (P - 1)) * D);
+            const uint8_t *kp = kbase + at, *vp = vbase + at;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < G::NJ; ++j)
+                    load_codes<16>(x.k[g][u][j], kp + 8 * u * D + 64 * j, live && (c + 4 * j) * 16 < D);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                load_codes<G::VB>(x.v[g][u], vp + ((u & 1) + 8 * (u >> 1)) * D, live && r * G::VB < D);
+            const uint64_t sc = (uint64_t)pg * scale_stride + (uint32_t)h;
+            x.ks[g] = __ldg(p.kv.ks + sc);
+            x.vs[g] = __ldg(p.kv.vs + sc);
+        }
+    };
+
+    // the first step's codes and the next one's pages are on their way while the queries
+    // are made ready
+    const int step = splits * WARPS;
+    int at_step = split * WARPS + warp, id[G::KG];
+    Codes<DP> x, y;
+    pages_of(at_step, id);
+    load(x, at_step, id);
+    pages_of(at_step + step, id);
 
     // queries of this lane: rows 8t + r, codes' dimensions (c + 4j) * 16 .. + 15
     uint32_t qh[NT][G::NJ][8], ql[NT][G::NJ][F32 ? 8 : 1];
@@ -218,209 +286,188 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !F32) ? 3 : 2) paged_a
         qf[t][1] = __shfl_sync(0xffffffffu, down, (2 * c + 1) * 4);
     }
 
-    float o[NT][G::VB / 2][4], mx[NT][2], sum[NT][2];
+    auto consume = [&](Codes<DP> &x, int i) {
+        const int k0 = key_of(i);
+        float s[G::KG][NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+        for (int g = 0; g < G::KG; ++g) {
 #pragma unroll
-        for (int i = 0; i < G::VB / 2; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
-        mx[t][0] = mx[t][1] = -INFINITY;
-        sum[t][0] = sum[t][1] = 0.f;
-    }
-    float ref = 0.f;                             // o counts in units of this value scale
-
-    const int32_t *table = p.pb.table + (int64_t)b * p.pb.table_stride;
-    const uint8_t *kbase = p.kv.k + (int64_t)h * P * D, *vbase = p.kv.v + (int64_t)h * P * D;
-    auto group_of = [&](int i) { return i < n_sink ? i : g_lo + i - n_sink; };
-    auto page_of = [&](int i) { return i < n_grp ? __ldg(table + ((group_of(i) << 4) >> p.kv.log2_page)) : 0; };
-    auto load = [&](Codes<DP> &x, int i, int id) {
-        int64_t pg = 0;
-        if (i < n_grp) pg = checked_page(id, p.kv, p.err);
-        const bool live = i < n_grp && pg >= 0;
-        if (!live) pg = 0;
-        const int at = (group_of(i) << 4) & (P - 1);
-        const uint8_t *kp = kbase + pg * p.kv.page_stride + (int64_t)at * D;
-        const uint8_t *vp = vbase + pg * p.kv.page_stride + (int64_t)at * D;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int t = 0; t < NT; ++t) s[g][t][0] = s[g][t][1] = s[g][t][2] = s[g][t][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < G::NJ; ++j)
-                load_codes<16>(x.k[u][j], kp + (r + 8 * u) * D + (c + 4 * j) * 16, live && (c + 4 * j) * 16 < D);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            load_codes<G::VB>(x.v[u], vp + (2 * c + (u & 1) + 8 * (u >> 1)) * D + r * G::VB, live && r * G::VB < D);
-        x.ks = live ? __ldg(p.kv.ks + pg * p.kv.scale_stride + h) : 1.f;
-        x.vs = live ? __ldg(p.kv.vs + pg * p.kv.scale_stride + h) : 1.f;
-    };
-
-    auto consume = [&](Codes<DP> &x, int i) {
-        const int k0 = group_of(i) << 4;
-        float s[NT][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < G::NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_f16(x.k[0][j][e], a0, a2);
-                e4m3x4_f16(x.k[1][j][e], a1, a3);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma16816(s[t], a0, a1, a2, a3, qh[t][j][2 * e], qh[t][j][2 * e + 1]);
-                    if constexpr (F32) mma16816(s[t], a0, a1, a2, a3, ql[t][j][2 * e], ql[t][j][2 * e + 1]);
-                }
-            }
-        // every row sees every key of the group?
-        const bool all = k0 + 15 <= p_lo && (p.window == 0 || k0 > p_hi - p.window || k0 + 15 < p.sinks);
-        float ratio = 1.f, shrink = 1.f;
-        if (x.vs != ref) {                       // same for the warp
-            if (x.vs > ref * 0x1p-24f) {
-                shrink = ref / x.vs;
-                ref = x.vs;
-            } else {
-                ratio = x.vs / ref;
-            }
-        }
-        uint32_t ph[NT][2], pl[NT][2], vis[NT][2];
-        float alpha[NT][2];
-        bool same = shrink == 1.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            uint32_t seen[4] = {1u, 1u, 1u, 1u};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] *= x.ks * qf[t][e & 1];
-            if (!all) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int key = k0 + r + 8 * (e >> 1);
-                    const int pos = sq.pos0 + (row0 + 8 * t + 2 * c + (e & 1)) / p.group;
-                    const bool see = key <= pos && (p.window == 0 || key > pos - p.window || key < p.sinks);
-                    seen[e] = see;
-                    if (!see) s[t][e] = -INFINITY;
-                }
-            }
-            vis[t][0] = seen[0] * 0x3c00u | seen[1] * 0x3c000000u;       // f16 ones
-            vis[t][1] = seen[2] * 0x3c00u | seen[3] * 0x3c000000u;
-            float m0 = fmaxf(s[t][0], s[t][2]), m1 = fmaxf(s[t][1], s[t][3]);
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_f16(x.k[g][0][j][e], a0, a2);
+                    e4m3x4_f16(x.k[g][1][j][e], a1, a3);
 #pragma unroll
-            for (int w = 4; w < 32; w <<= 1) {
-                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, w));
-                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, w));
-            }
-            m0 = fmaxf(m0, mx[t][0]);
-            m1 = fmaxf(m1, mx[t][1]);
-            // a row that has seen nothing yet subtracts 0 from scores that are all -inf
-            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-            alpha[t][0] = exp2_approx(mx[t][0] - u0);
-            alpha[t][1] = exp2_approx(mx[t][1] - u1);
-            mx[t][0] = m0;
-            mx[t][1] = m1;
-            const float e0 = exp2_approx(s[t][0] - u0 + P_BIAS), e1 = exp2_approx(s[t][1] - u1 + P_BIAS);
-            const float e2 = exp2_approx(s[t][2] - u0 + P_BIAS), e3 = exp2_approx(s[t][3] - u1 + P_BIAS);
-            sum[t][0] = sum[t][0] * alpha[t][0] + (e0 + e2);
-            sum[t][1] = sum[t][1] * alpha[t][1] + (e1 + e3);
-            const float w0 = e0 * ratio, w1 = e1 * ratio, w2 = e2 * ratio, w3 = e3 * ratio;
-            ph[t][0] = pack_f16(w0, w1);
-            ph[t][1] = pack_f16(w2, w3);
-            if constexpr (F32) {
-                pl[t][0] = transpose8x8(pack_f16_rest(w0, w1, ph[t][0]));
-                pl[t][1] = transpose8x8(pack_f16_rest(w2, w3, ph[t][1]));
-            }
-            ph[t][0] = transpose8x8(ph[t][0]);
-            ph[t][1] = transpose8x8(ph[t][1]);
-            same = same && alpha[t][0] == 1.f && alpha[t][1] == 1.f;
+                    for (int t = 0; t < NT; ++t) {
+                        mma16816(s[g][t], a0, a1, a2, a3, qh[t][j][2 * e], qh[t][j][2 * e + 1]);
+                        if constexpr (F32) mma16816(s[g][t], a0, a1, a2, a3, ql[t][j][2 * e], ql[t][j][2 * e + 1]);
+                    }
+                }
         }
-        if (!__all_sync(0xffffffffu, same)) {
+        // every row sees every key of the step?
+        const bool all = k0 + G::KEYS - 1 <= p_lo && (p.window == 0 || k0 > p_hi - p.window || k0 + G::KEYS - 1 < p.sinks);
+        bool grow = false;
+        float top[NT][2];
+        uint32_t vis[G::KG][NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            top[t][0] = top[t][1] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < G::KG; ++g) {
+                const float f0 = x.ks[g] * qf[t][0], f1 = x.ks[g] * qf[t][1];
+                s[g][t][0] *= f0, s[g][t][2] *= f0;
+                s[g][t][1] *= f1, s[g][t][3] *= f1;
+                if (!all) {
+                    vis[g][t][0] = vis[g][t][1] = 0u;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = k0 + 16 * g + r + 8 * (e >> 1);
+                        const int pos = sq.pos0 + (row0 + 8 * t + 2 * c + (e & 1)) / p.group;
+                        const bool see = key <= pos && (p.window == 0 || key > pos - p.window || key < p.sinks);
+                        vis[g][t][e >> 1] |= see ? (e & 1 ? 0x3c000000u : 0x3c00u) : 0u;             // f16 ones
+                        if (!see) s[g][t][e] = -INFINITY;
+                    }
+                }
+                top[t][0] = fmaxf(top[t][0], fmaxf(s[g][t][0], s[g][t][2]));
+                top[t][1] = fmaxf(top[t][1], fmaxf(s[g][t][1], s[g][t][3]));
+            }
+            grow = grow || top[t][0] > mx[t][0] + LAZY || top[t][1] > mx[t][1] + LAZY;
+        }
+        // The maximum moves only when some row's grew by more than 2^LAZY: one vote a step
+        // instead of three exchanges a row, and hardly ever a rescaling.
+        if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const float f0 = alpha[t][0] * shrink, f1 = alpha[t][1] * shrink;
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = top[t][e];
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                    f[e] = 1.f;
+                    if (m > mx[t][e] + LAZY) {
+                        f[e] = exp2_approx(mx[t][e] - m);
+                        mx[t][e] = m;
+                    }
+                    sum[t][e] *= f[e];
+                }
 #pragma unroll
                 for (int d = 0; d < G::VB / 2; ++d) {
-                    o[t][d][0] *= f0, o[t][d][2] *= f0;
-                    o[t][d][1] *= f1, o[t][d][3] *= f1;
+                    o[t][d][0] *= f[0], o[t][d][2] *= f[0];
+                    o[t][d][1] *= f[1], o[t][d][3] *= f[1];
                 }
             }
         }
-        if (!all) {
-            // A NaN value must reach the rows that see its key and no other: take the
-            // NaN codes out, and where there are any, count for each row and dimension
-            // the ones it sees (the same product with ones in place of the weights).
-            uint32_t any = 0, bad[4][DP / 32];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+        for (int g = 0; g < G::KG; ++g) {
+            // the unit of o: the largest value scale so far, or a smaller one where the step's is
+            // so small that its weights would lose bits in f16
+            const float vs = x.vs[g];
+            if (vs > ref || (vs < ref * 0x1p-12f && vs > ref * 0x1p-60f)) {       // same for the warp
+                const float shrink = ref / vs;
+                ref = vs;
+                inv_ref = 1.f / vs;
 #pragma unroll
-                for (int w = 0; w < DP / 32; ++w) {
-                    bad[u][w] = nan_bytes(x.v[u][w]);
-                    any |= bad[u][w];
-                    x.v[u][w] &= ~bad[u][w];
-                    bad[u][w] &= 0x38383838u;    // e4m3 one
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int d = 0; d < G::VB / 2; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[t][d][e] *= shrink;
+            }
+            const float ratio = vs * inv_ref;
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                // a row that has seen nothing yet subtracts 0 from scores that are all -inf
+                const float u0 = (mx[t][0] == -INFINITY ? 0.f : mx[t][0]) - P_BIAS;
+                const float u1 = (mx[t][1] == -INFINITY ? 0.f : mx[t][1]) - P_BIAS;
+                const float e0 = exp2_approx(s[g][t][0] - u0), e1 = exp2_approx(s[g][t][1] - u1);
+                const float e2 = exp2_approx(s[g][t][2] - u0), e3 = exp2_approx(s[g][t][3] - u1);
+                sum[t][0] += e0 + e2;
+                sum[t][1] += e1 + e3;
+                const float w0 = e0 * ratio, w1 = e1 * ratio, w2 = e2 * ratio, w3 = e3 * ratio;
+                ph[t][0] = pack_f16(w0, w1);
+                ph[t][1] = pack_f16(w2, w3);
+                if constexpr (F32) {
+                    pl[t][0] = transpose8x8(pack_f16_rest(w0, w1, ph[t][0]));
+                    pl[t][1] = transpose8x8(pack_f16_rest(w2, w3, ph[t][1]));
                 }
-            if (__any_sync(0xffffffffu, any != 0)) {
+                ph[t][0] = transpose8x8(ph[t][0]);
+                ph[t][1] = transpose8x8(ph[t][1]);
+            }
+            if (!all) {
+                // A NaN value must reach the rows that see its key and no other: take the
+                // NaN codes out, and where there are any, count for each row and dimension
+                // the ones it sees (the same product with ones in place of the weights).
+                uint32_t any = 0, bad[4][DP / 32];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int w = 0; w < DP / 32; ++w) {
+                        bad[u][w] = nan_bytes(x.v[g][u][w]);
+                        any |= bad[u][w];
+                        x.v[g][u][w] &= ~bad[u][w];
+                        bad[u][w] &= 0x38383838u;    // e4m3 one
+                    }
+                if (__any_sync(0xffffffffu, any != 0)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t b0 = transpose8x8(vis[g][t][0]), b1 = transpose8x8(vis[g][t][1]);
+#pragma unroll
+                        for (int d = 0; d < G::VB / 2; ++d) {
+                            float n[4] = {};
+                            const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2, sh = 8 * (d & 3);
+                            auto pair = [&](int u, int w) {
+                                uint32_t lo, hi;
+                                e4m3x4_f16(((bad[u][w] >> sh) & 0xffu) | (((bad[u + 1][w] >> sh) & 0xffu) << 8), lo, hi);
+                                return lo;
+                            };
+                            mma16816(n, pair(0, w0), pair(0, w1), pair(2, w0), pair(2, w1), b0, b1);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n[e] > 0.f) o[t][d][e] = __int_as_float(0x7fffffff);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < G::VB / 2; d += 2) {
+                // dimensions r * VB + d, d + 1 (rows r) and + VB / 2 (rows r + 8)
+                const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2;
+                const uint32_t pick = (d & 2) ? 0x7362u : 0x5140u;
+                uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
+                e4m3x4_f16(__byte_perm(x.v[g][0][w0], x.v[g][1][w0], pick), a0, e0);
+                e4m3x4_f16(__byte_perm(x.v[g][0][w1], x.v[g][1][w1], pick), a1, e1);
+                e4m3x4_f16(__byte_perm(x.v[g][2][w0], x.v[g][3][w0], pick), a2, e2);
+                e4m3x4_f16(__byte_perm(x.v[g][2][w1], x.v[g][3][w1], pick), a3, e3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const uint32_t b0 = transpose8x8(vis[t][0]), b1 = transpose8x8(vis[t][1]);
-#pragma unroll
-                    for (int d = 0; d < G::VB / 2; ++d) {
-                        float n[4] = {};
-                        const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2, sh = 8 * (d & 3);
-                        auto pair = [&](int u, int w) {
-                            uint32_t lo, hi;
-                            e4m3x4_f16(((bad[u][w] >> sh) & 0xffu) | (((bad[u + 1][w] >> sh) & 0xffu) << 8), lo, hi);
-                            return lo;
-                        };
-                        mma16816(n, pair(0, w0), pair(0, w1), pair(2, w0), pair(2, w1), b0, b1);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n[e] > 0.f) o[t][d][e] = __int_as_float(0x7fffffff);
+                    mma16816(o[t][d], a0, a1, a2, a3, ph[t][0], ph[t][1]);
+                    mma16816(o[t][d + 1], e0, e1, e2, e3, ph[t][0], ph[t][1]);
+                    if constexpr (F32) {
+                        mma16816(o[t][d], a0, a1, a2, a3, pl[t][0], pl[t][1]);
+                        mma16816(o[t][d + 1], e0, e1, e2, e3, pl[t][0], pl[t][1]);
                     }
                 }
             }
         }
-#pragma unroll
-        for (int d = 0; d < G::VB / 2; d += 2) {
-            // dimensions r * VB + d, d + 1 (rows r) and + VB / 2 (rows r + 8)
-            const int w0 = d >> 2, w1 = (d + G::VB / 2) >> 2;
-            const uint32_t pick = (d & 2) ? 0x7362u : 0x5140u;
-            const uint32_t x0 = __byte_perm(x.v[0][w0], x.v[1][w0], pick), x1 = __byte_perm(x.v[0][w1], x.v[1][w1], pick);
-            const uint32_t x2 = __byte_perm(x.v[2][w0], x.v[3][w0], pick), x3 = __byte_perm(x.v[2][w1], x.v[3][w1], pick);
-            uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
-            e4m3x4_f16(x0, a0, e0);
-            e4m3x4_f16(x1, a1, e1);
-            e4m3x4_f16(x2, a2, e2);
-            e4m3x4_f16(x3, a3, e3);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma16816(o[t][d], a0, a1, a2, a3, ph[t][0], ph[t][1]);
-                mma16816(o[t][d + 1], e0, e1, e2, e3, ph[t][0], ph[t][1]);
-                if constexpr (F32) {
-                    mma16816(o[t][d], a0, a1, a2, a3, pl[t][0], pl[t][1]);
-                    mma16816(o[t][d + 1], e0, e1, e2, e3, pl[t][0], pl[t][1]);
-                }
-            }
-        }
     };
 
-    // groups are dealt round-robin to the warps of the cluster; the next group's codes
-    // are on their way while one is worked on, and the page number after that
-    {
-        const int step = splits * WARPS;
-        int i = split * WARPS + warp;
-        Codes<DP> x, y;
-        load(x, i, page_of(i));
-        int id = page_of(i + step);
-        while (i < n_grp) {
-            load(y, i + step, id);
-            id = page_of(i + 2 * step);
-            consume(x, i);
-            i += step;
-            if (i >= n_grp) break;
-            load(x, i + step, id);
-            id = page_of(i + 2 * step);
-            consume(y, i);
-            i += step;
-        }
+    // steps are dealt round-robin to the warps of the cluster; the next step's codes are on
+    // their way while one is worked on, and the page numbers after that
+    for (int i = at_step; i < n_grp;) {
+        load(y, i + step, id);
+        pages_of(i + 2 * step, id);
+        consume(x, i);
+        i += step;
+        if (i >= n_grp) break;
+        load(x, i + step, id);
+        pages_of(i + 2 * step, id);
+        consume(y, i);
+        i += step;
     }
 
     // shares of this warp to shared memory: o in units of 2^-P_BIAS, as is the sum
@@ -508,30 +555,24 @@ caat_status launch_few(AttnParams &p, cudaStream_t s)
     const int64_t units = (int64_t)p.pb.batch * p.kv.kv_heads * chunks;
     if (chunks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     p.chunks = (int)chunks;
-    // blocks for each unit: enough to fill the SMs twice, while each warp still gets two
-    // groups of 16 keys of the longest sequence the page table can hold
+    // blocks for each unit: enough to fill the SMs, while each warp still gets four steps of
+    // the longest sequence the page table can hold
     int64_t keys = (int64_t)p.pb.width * p.kv.page;
     if (p.window > 0 && keys > (int64_t)p.window + p.sinks + p.pb.q_max) keys = (int64_t)p.window + p.sinks + p.pb.q_max;
     int splits = 1;
-    while (splits < 16 && units * splits < 6 * (int64_t)num_sms() && keys > (int64_t)splits * WARPS * 32) splits *= 2;
+    while (splits < 8 && units * splits < 4 * (int64_t)num_sms() && keys > (int64_t)splits * WARPS * G::KEYS * 4) splits *= 2;
     if (units * splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     auto kern = paged_attn_few_kernel<DP, NT, F32>;
     const int smem = (WARPS + 1) * G::ROWS * G::PART * 4;
     if (prepare_kernel_smem((const void *)kern, smem) != CAAT_OK) return CAAT_ERR_CUDA;
-    if (splits > 8 && cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                          cudaSuccess)
-        return CAAT_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(units * splits));
     cfg.blockDim = dim3(WARPS * 32);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
+    cfg.numAttrs = serve_attrs(attr, splits);
     if (cudaLaunchKernelEx(&cfg, kern, p, splits) != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("paged_attn_few");
     return CAAT_OK;

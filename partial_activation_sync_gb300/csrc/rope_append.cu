@@ -18,6 +18,7 @@
 // holds 16 values of one token row (a pair slot), so both halves of every rotated
 // pair and the 16-byte store of the codes are its own.
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace caat {
 namespace {
@@ -162,6 +163,8 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) rope_append_kernel(AppendPa
     const int slot = (int)(rest % slots_per_seq), b = (int)(rest / slots_per_seq);
     const int P = p.kv.page, D = p.kv.dim, SL = D / 16, G = p.kv.kv_heads;
 
+    tc::griddep_wait();                      // for the previous launch, before the first access
+    tc::griddep_launch_dependents();
     const Seq sq = load_seq(p.pb, P, b, p.err);
     if (sq.n == 0) return;
     // tokens of this team: those of page j of the sequence (page 0 also gets the
@@ -266,13 +269,14 @@ caat_status launch(const AppendParams &p, cudaStream_t s)
         const int64_t teams = (int64_t)p.pb.batch * slots * jobs;
         const int64_t blocks = (teams + 3) / 4;
         if (blocks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
-        rope_append_kernel<E, INTER, true><<<(unsigned)blocks, 128, 0, s>>>(p, slots, 1, jobs, teams);
+        launch_dependent(rope_append_kernel<E, INTER, true>, dim3((unsigned)blocks), dim3(128), 0, s, p, slots, 1, jobs, teams);
     } else {
         const int threads = (tokens * SL + 31) / 32 * 32;
         const int jobs_per = 1, chunks = (jobs + jobs_per - 1) / jobs_per;
         const int64_t blocks = (int64_t)p.pb.batch * slots * chunks;
         if (blocks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
-        rope_append_kernel<E, INTER, false><<<(unsigned)blocks, threads, 0, s>>>(p, slots, jobs_per, chunks, blocks);
+        launch_dependent(rope_append_kernel<E, INTER, false>, dim3((unsigned)blocks), dim3((unsigned)threads), 0, s, p, slots,
+                         jobs_per, chunks, blocks);
     }
     if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("rope_append");

@@ -30,6 +30,7 @@
 // Bound by the instructions of those passes for large vocabularies and by the latency
 // of the chain for few rows.
 #include "paged.cuh"
+#include "tc_ptx.cuh"
 
 namespace caat {
 namespace {
@@ -267,6 +268,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
     const int V = (int)p.V;
     const int seg = (V + WARPS - 1) / WARPS, lo = min(V, warp * seg), hi = min(V, lo + seg);   // this warp's run
 
+    tc::griddep_wait();                      // for the previous launch, before the first access
+    tc::griddep_launch_dependents();
     // the thread's and the row's largest value (fmaxf passes over NaN)
     float top = -INFINITY;
     each(z, lo, hi, lane, 32, [&](int, float x) { top = fmaxf(top, x); });
@@ -605,7 +608,7 @@ caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
 {
     auto kern = sample_kernel<E>;
     if (prepare_kernel_smem((const void *)kern, (int)sizeof(Shared)) != CAAT_OK) return CAAT_ERR_CUDA;
-    kern<<<(unsigned)B, THREADS, sizeof(Shared), s>>>(p);
+    launch_dependent(kern, dim3((unsigned)B), dim3(THREADS), sizeof(Shared), s, p);
     if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("sample_tokens");
     return CAAT_OK;

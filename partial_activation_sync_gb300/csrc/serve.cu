@@ -40,8 +40,9 @@ bool make_kv(const caat_paged_kv *a, PagedKV &kv)
     if (a == nullptr || a->pages < 1 || a->pages > 0x7fffffff || a->kv_heads < 1 || a->kv_heads > 65536) return false;
     if (a->page != 16 && a->page != 32 && a->page != 64 && a->page != 128) return false;
     if (a->dim < 16 || a->dim > 128 || a->dim % 16 != 0) return false;
-    if (a->scale_stride < a->kv_heads || a->scale_stride > ((int64_t)1 << 48)) return false;
-    if (a->page_stride < (int64_t)a->kv_heads * a->page * a->dim) return false;
+    // the kernels multiply page numbers by 32-bit strides, into 64 bits
+    if (a->scale_stride < a->kv_heads || a->scale_stride > 0xffffffffll) return false;
+    if (a->page_stride < (int64_t)a->kv_heads * a->page * a->dim || a->page_stride > 0xffffffffll) return false;
     if (!good_strided(a->k, 1, {a->page_stride}) || !good_strided(a->v, 1, {a->page_stride})) return false;
     if (a->k_scale == nullptr || a->v_scale == nullptr) return false;
     const int log2_page = a->page == 16 ? 4 : a->page == 32 ? 5 : a->page == 64 ? 6 : 7;
@@ -86,6 +87,24 @@ int *serve_error_word()
         __atomic_store_n(&cached[dev], p, __ATOMIC_RELEASE);
     }
     return p;
+}
+
+unsigned serve_attrs(cudaLaunchAttribute (&attr)[2], int cluster)
+{
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    const char *env = std::getenv("CAAT_PDL");
+    if (env == nullptr || std::strcmp(env, "0") != 0) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    return n;
 }
 
 caat_status read_and_clear_serve_error()

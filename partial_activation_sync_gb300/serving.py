@@ -11,20 +11,22 @@ import ctypes
 from . import _check, _dtype_code, _lib, _stream_ptr, _torch
 
 
-def _strides(x, last, shape, dtype, name):
+def _strides(x, shape, dtype, name):
     """Strides of a CUDA tensor of that shape and dtype whose last dimension is dense."""
-    if tuple(x.shape) != shape or x.dtype != dtype or not x.is_cuda:
-        raise ValueError("caat: %s must be a CUDA tensor %s of dtype %s" % (name, list(shape), dtype))
     st = x.stride()
-    if st[-1] != 1 and last > 1:
-        raise ValueError("caat: the last dimension of %s must be dense" % name)
+    if x.shape != shape or x.dtype != dtype or not x.is_cuda or st[-1] != 1:
+        raise ValueError("caat: %s must be a CUDA tensor %s of dtype %s, its last dimension dense" % (name, list(shape), dtype))
     return st
 
 
 def _vector(x, n, dtype, name):
-    if x.dtype != dtype or tuple(x.shape) != (n,) or not x.is_cuda or (n > 1 and x.stride(0) != 1):
+    if x.dtype != dtype or x.shape != (n,) or not x.is_cuda or (n > 1 and x.stride(0) != 1):
         raise ValueError("caat: %s must be a dense CUDA tensor [%d] of dtype %s" % (name, n, dtype))
-    return ctypes.c_void_p(x.data_ptr())
+    return x.data_ptr()
+
+
+def _stream(stream, like):
+    return _stream_ptr(stream, like).value or 0
 
 
 class PagedKVCache:
@@ -133,8 +135,8 @@ def rope_append(q, k, v, cos, sin, cache, batch, interleaved=False, q_out=None, 
     may be ``q``, allocated when None)."""
     torch = _torch()
     T, H, q_st, q_sk, q_sg = _queries(q, cache)
-    kst = _strides(k, cache.dim, (T, cache.kv_heads, cache.dim), q.dtype, "k")
-    vst = _strides(v, cache.dim, (T, cache.kv_heads, cache.dim), q.dtype, "v")
+    kst = _strides(k, (T, cache.kv_heads, cache.dim), q.dtype, "k")
+    vst = _strides(v, (T, cache.kv_heads, cache.dim), q.dtype, "v")
     dt = _dtype_code(q)
     if (cos is None) != (sin is None):
         raise ValueError("caat: cos and sin are given together")
@@ -142,18 +144,18 @@ def rope_append(q, k, v, cos, sin, cache, batch, interleaved=False, q_out=None, 
     if cos is not None:
         positions, rot = cos.shape[0], 2 * cos.shape[1]
         for x, name in ((cos, "cos"), (sin, "sin")):
-            if tuple(x.shape) != (positions, rot // 2) or x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
+            if x.shape != (positions, rot // 2) or x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
                 raise ValueError("caat: %s must be a dense CUDA tensor [positions, rot / 2] of dtype torch.float32" % name)
-        cp, sp = ctypes.c_void_p(cos.data_ptr()), ctypes.c_void_p(sin.data_ptr())
+        cp, sp = cos.data_ptr(), sin.data_ptr()
     if q_out is None:
         q_out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
-    ost = _strides(q_out, cache.dim, (T, H, cache.dim), q.dtype, "q_out")
+    ost = _strides(q_out, (T, H, cache.dim), q.dtype, "q_out")
     batch._c.tokens = T
     st = _lib.load().caat_rope_append(
-        cache._ref, batch._ref, H, dt, ctypes.c_void_p(q.data_ptr()), q_st, q_sk, q_sg,
-        ctypes.c_void_p(k.data_ptr()), kst[0], kst[1], ctypes.c_void_p(v.data_ptr()), vst[0], vst[1],
-        cp, sp, positions, rot, 1 if interleaved else 0, ctypes.c_void_p(q_out.data_ptr()), ost[0], ost[1],
-        _stream_ptr(stream, q))
+        cache._ref, batch._ref, H, dt, q.data_ptr(), q_st, q_sk, q_sg,
+        k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
+        cp, sp, positions, rot, 1 if interleaved else 0, q_out.data_ptr(), ost[0], ost[1],
+        _stream(stream, q))
     _check(st, "caat_rope_append")
     return q_out
 
@@ -170,12 +172,12 @@ def paged_attention(q, cache, batch, softmax_scale=None, window=0, sinks=0, out=
     dt = _dtype_code(q)
     if out is None:
         out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
-    ost = _strides(out, cache.dim, (T, H, cache.dim), q.dtype, "out")
+    ost = _strides(out, (T, H, cache.dim), q.dtype, "out")
     batch._c.tokens = T
     st = _lib.load().caat_paged_attention(
-        cache._ref, batch._ref, H, dt, ctypes.c_void_p(q.data_ptr()), q_st, q_sk, q_sg,
+        cache._ref, batch._ref, H, dt, q.data_ptr(), q_st, q_sk, q_sg,
         cache.dim ** -0.5 if softmax_scale is None else float(softmax_scale), int(window), int(sinks),
-        ctypes.c_void_p(out.data_ptr()), ost[0], ost[1], _stream_ptr(stream, q))
+        out.data_ptr(), ost[0], ost[1], _stream(stream, q))
     _check(st, "caat_paged_attention")
     return out
 
@@ -199,9 +201,9 @@ def sample_tokens(logits, u, temperature, top_k, top_p, min_p, tokens=None, logp
     if logprobs is None:
         logprobs = torch.empty(B, dtype=f32, device=logits.device)
     st = _lib.load().caat_sample_tokens(
-        B, V, _dtype_code(logits), ctypes.c_void_p(logits.data_ptr()), logits.stride(0) if B > 1 else V,
+        B, V, _dtype_code(logits), logits.data_ptr(), logits.stride(0) if B > 1 else V,
         _vector(u, B, f32, "u"), _vector(temperature, B, f32, "temperature"), _vector(top_k, B, i32, "top_k"),
         _vector(top_p, B, f32, "top_p"), _vector(min_p, B, f32, "min_p"), _vector(tokens, B, i32, "tokens"),
-        _vector(logprobs, B, f32, "logprobs"), _stream_ptr(stream, logits))
+        _vector(logprobs, B, f32, "logprobs"), _stream(stream, logits))
     _check(st, "caat_sample_tokens")
     return tokens, logprobs
