@@ -74,23 +74,15 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t p
     return pack_f16(lo - f.x, hi - f.y);
 }
 
-// B = 16 or 8 codes of one row, read once; zeros unless `live`.  Predicated, not
-// branched around: the loads of a group are then all in flight together.
-template <int B>
-__device__ __forceinline__ void load_codes(uint32_t (&w)[B / 4], const uint8_t *p, bool live)
+template <int B>                     // B = 16 or 8 codes of one row, read once
+__device__ __forceinline__ void load_codes(uint32_t (&w)[B / 4], const uint8_t *p)
 {
-#pragma unroll
-    for (int i = 0; i < B / 4; ++i) w[i] = 0;
     if constexpr (B == 16) {
-        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                     "@q ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                     : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3])
-                     : "l"(p), "r"((uint32_t)live));
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "l"(p));
     } else {
-        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
-                     "@q ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
-                     : "+r"(w[0]), "+r"(w[1])
-                     : "l"(p), "r"((uint32_t)live));
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     }
 }
 
@@ -176,41 +168,55 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<DP, NT, F32>::MIN_BLOCKS) page
 
     const int32_t *table = p.pb.table + (int64_t)b * p.pb.table_stride;
     const int64_t head = (int64_t)h * P * D;
-    const uint8_t *kbase = p.kv.k + head + r * D + c * 16, *vbase = p.kv.v + head + 2 * c * D + r * G::VB;
+    // Lanes beyond the head dimension repeat chunk 0 (unconditional loads): its products meet
+    // query zeros, and output dimensions that are not written.
+    const uint8_t *kbase = p.kv.k + head + r * D, *vbase = p.kv.v + head + 2 * c * D + (r * G::VB < D ? r * G::VB : 0);
+    uint32_t kchunk[G::NJ];
+#pragma unroll
+    for (int j = 0; j < G::NJ; ++j) kchunk[j] = (c + 4 * j) * 16 < D ? (c + 4 * j) * 16 : 0;
     const uint32_t page_stride = (uint32_t)p.kv.page_stride, scale_stride = (uint32_t)p.kv.scale_stride;
     auto key_of = [&](int i) { return (i < n_sink ? i : g_lo + i - n_sink) << G::LOG_KEYS; };
-    // pages of a step's groups (16 keys lie within a page)
+    // pages of a step's groups (16 keys lie within a page); groups beyond the last visible key
+    // read page 0, whose codes the mask and the NaN check keep out
+    // Steps past the last repeat it: loads without a branch or a predicate are all in flight
+    // together, and the codes of the last step are in L2.
     auto pages_of = [&](int i, int (&id)[G::KG]) {
+        i = min(i, n_grp - 1);
 #pragma unroll
         for (int g = 0; g < G::KG; ++g) {
             const int key = key_of(i) + 16 * g;
-            id[g] = i < n_grp && key <= p_hi ? __ldg(table + (key >> p.kv.log2_page)) : 0;
+            if (g > 0 && P > 16) id[g] = id[0];  // one page holds the whole step
+            else id[g] = key <= p_hi ? __ldg(table + (key >> p.kv.log2_page)) : 0;
         }
     };
     auto load = [&](Codes<DP> &x, int i, const int (&id)[G::KG]) {
+        i = min(i, n_grp - 1);
 #pragma unroll
         for (int g = 0; g < G::KG; ++g) {
             const int key = key_of(i) + 16 * g;
-            bool live = i < n_grp && key <= p_hi;
             uint32_t pg = (uint32_t)id[g];
-            if (pg >= (uint32_t)p.kv.pages) {    // no such page: nothing is read for it
-                if (live) *(volatile int *)p.err = CAAT_ERR_INVALID_ARG;
-                live = false;
+            if (pg >= (uint32_t)p.kv.pages) {
+                *(volatile int *)p.err = CAAT_ERR_INVALID_ARG;
                 pg = 0;
             }
             const uint64_t at = (uint64_t)pg * page_stride + (uint32_t)((key & (P - 1)) * D);
-            const uint8_t *kp = kbase + at, *vp = vbase + at;
+            const uint8_t *kp = kbase + at, *vp = vbase + at, *kp8 = kp + 8 * D, *vp8 = vp + 8 * D;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int j = 0; j < G::NJ; ++j)
-                    load_codes<16>(x.k[g][u][j], kp + 8 * u * D + 64 * j, live && (c + 4 * j) * 16 < D);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                load_codes<G::VB>(x.v[g][u], vp + ((u & 1) + 8 * (u >> 1)) * D, live && r * G::VB < D);
-            const uint64_t sc = (uint64_t)pg * scale_stride + (uint32_t)h;
-            x.ks[g] = __ldg(p.kv.ks + sc);
-            x.vs[g] = __ldg(p.kv.vs + sc);
+            for (int j = 0; j < G::NJ; ++j) {
+                load_codes<16>(x.k[g][0][j], kp + kchunk[j]);
+                load_codes<16>(x.k[g][1][j], kp8 + kchunk[j]);
+            }
+            load_codes<G::VB>(x.v[g][0], vp);
+            load_codes<G::VB>(x.v[g][1], vp + D);
+            load_codes<G::VB>(x.v[g][2], vp8);
+            load_codes<G::VB>(x.v[g][3], vp8 + D);
+            if (g > 0 && P > 16) {
+                x.ks[g] = x.ks[0], x.vs[g] = x.vs[0];
+            } else {
+                const uint64_t sc = (uint64_t)pg * scale_stride + (uint32_t)h;
+                x.ks[g] = __ldg(p.kv.ks + sc);
+                x.vs[g] = __ldg(p.kv.vs + sc);
+            }
         }
     };
 
@@ -219,9 +225,11 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<DP, NT, F32>::MIN_BLOCKS) page
     const int step = splits * WARPS;
     int at_step = split * WARPS + warp, id[G::KG];
     Codes<DP> x, y;
-    pages_of(at_step, id);
-    load(x, at_step, id);
-    pages_of(at_step + step, id);
+    if (n_grp > 0) {
+        pages_of(at_step, id);
+        load(x, at_step, id);
+        pages_of(at_step + step, id);
+    }
 
     // queries of this lane: rows 8t + r, codes' dimensions (c + 4j) * 16 .. + 15
     uint32_t qh[NT][G::NJ][8], ql[NT][G::NJ][F32 ? 8 : 1];
@@ -363,6 +371,7 @@ __global__ void __launch_bounds__(WARPS * 32, Geo<DP, NT, F32>::MIN_BLOCKS) page
         }
 #pragma unroll
         for (int g = 0; g < G::KG; ++g) {
+            if (g > 0 && k0 + 16 * g > p_hi) break;       // nothing of the sequence there
             // the unit of o: the largest value scale so far, or a smaller one where the step's is
             // so small that its weights would lose bits in f16
             const float vs = x.vs[g];
@@ -555,12 +564,13 @@ caat_status launch_few(AttnParams &p, cudaStream_t s)
     const int64_t units = (int64_t)p.pb.batch * p.kv.kv_heads * chunks;
     if (chunks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     p.chunks = (int)chunks;
-    // blocks for each unit: enough to fill the SMs, while each warp still gets four steps of
-    // the longest sequence the page table can hold
+    // Blocks for each unit: as many as are resident together (a second wave of 64 units in 8
+    // blocks each took 19.6 us against 14.9 in 4), while each warp still gets four steps of the
+    // longest sequence the page table can hold.
     int64_t keys = (int64_t)p.pb.width * p.kv.page;
     if (p.window > 0 && keys > (int64_t)p.window + p.sinks + p.pb.q_max) keys = (int64_t)p.window + p.sinks + p.pb.q_max;
     int splits = 1;
-    while (splits < 8 && units * splits < 4 * (int64_t)num_sms() && keys > (int64_t)splits * WARPS * G::KEYS * 4) splits *= 2;
+    while (splits < 8 && 2 * units * splits <= G::MIN_BLOCKS * (int64_t)num_sms() && keys > (int64_t)splits * WARPS * G::KEYS * 4) splits *= 2;
     if (units * splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
     auto kern = paged_attn_few_kernel<DP, NT, F32>;
     const int smem = (WARPS + 1) * G::ROWS * G::PART * 4;
