@@ -35,7 +35,7 @@
 namespace caat {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, BINS = 32;
+constexpr int BINS = 32;
 constexpr int CAP = 2048;                       // values that are sorted in shared memory
 constexpr float FLT_BIG = 3.402823466e38f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -71,42 +71,45 @@ __device__ __forceinline__ float value(const __nv_bfloat16 *p, int i)
 }
 
 // f(index, logit) for every element of [lo, hi), shared out over `team` threads: 16-byte
-// loads, four in flight, between an unaligned head and tail.  Threads call f a different
+// loads, two in flight, between an unaligned head and tail.  Threads call f a different
 // number of times.
 template <typename E, typename F>
 __device__ __forceinline__ void each(const E *z, int lo, int hi, int me, int team, F f)
 {
-    constexpr int N = 16 / sizeof(E), U = 4;
+    constexpr int N = 16 / sizeof(E);
     const int off = (int)(((16 - ((uintptr_t)(z + lo) & 15)) & 15) / sizeof(E));
     const int a = min(hi, lo + off), vecs = (hi - a) / N, b = a + vecs * N;
-    for (int i = lo + me; i < a; i += team) f(i, value(z, i));
+    // head and tail: fewer than N elements each
+    {
+        const int i = me < N ? lo + me : b + me - N;
+        const bool in = me < N ? i < a : i < hi;
+        if (me < 2 * N && in) f(i, value(z, i));
+    }
     const uint4 *v = reinterpret_cast<const uint4 *>(z + a);
-    for (int i = me; i < vecs; i += U * team) {
-        uint4 w[U];
+    uint4 w = make_uint4(0, 0, 0, 0), next = w;
+    if (me < vecs) w = __ldg(v + me);
+    if (me + team < vecs) next = __ldg(v + me + team);
+#pragma unroll 1
+    for (int i = me; i < vecs; i += team) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        w = next;
+        if (i + 2 * team < vecs) next = __ldg(v + i + 2 * team);
+        const int at = a + i * N;
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-            if (i + k * team < vecs) w[k] = __ldg(v + i + k * team);
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i + k * team >= vecs) break;
-            const int at = a + (i + k * team) * N;
-            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (N == 8) {
-                    f(at + 2 * e, __uint_as_float(x[e] << 16));
-                    f(at + 2 * e + 1, __uint_as_float(x[e] & 0xffff0000u));
-                } else {
-                    f(at + e, __uint_as_float(x[e]));
-                }
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (N == 8) {
+                f(at + 2 * e, __uint_as_float(x[e] << 16));
+                f(at + 2 * e + 1, __uint_as_float(x[e] & 0xffff0000u));
+            } else {
+                f(at + e, __uint_as_float(x[e]));
             }
         }
     }
-    for (int i = b + me; i < hi; i += team) f(i, value(z, i));
 }
 
 typedef unsigned long long u64;
 
+template <int WARPS>
 struct Shared {
     u64 list[CAP];
     float bins[WARPS][BINS][32];
@@ -120,7 +123,8 @@ constexpr float ONE = 1099511627776.f;          // 2^40: a weight of 1
 
 __device__ __forceinline__ u64 fixed(float w) { return (u64)(w * ONE); }
 
-__device__ __forceinline__ u64 block_sum(u64 x, Shared &sh)
+template <int WARPS>
+__device__ __forceinline__ u64 block_sum(u64 x, Shared<WARPS> &sh)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -129,12 +133,13 @@ __device__ __forceinline__ u64 block_sum(u64 x, Shared &sh)
     __syncthreads();
     x = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return __shfl_sync(0xffffffffu, x, 0);
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
 
 // sum of the values of the threads below this one, and of all
-__device__ __forceinline__ u64 block_scan(u64 x, Shared &sh, u64 &all)
+template <int WARPS>
+__device__ __forceinline__ u64 block_scan(u64 x, Shared<WARPS> &sh, u64 &all)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 inc = x;
@@ -157,7 +162,8 @@ __device__ __forceinline__ u64 block_scan(u64 x, Shared &sh, u64 &all)
     return below + inc - x;
 }
 
-__device__ __forceinline__ u64 block_max(u64 x, Shared &sh)
+template <int WARPS>
+__device__ __forceinline__ u64 block_max(u64 x, Shared<WARPS> &sh)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -166,20 +172,21 @@ __device__ __forceinline__ u64 block_max(u64 x, Shared &sh)
     __syncthreads();
     x = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return __shfl_sync(0xffffffffu, x, 0);
+    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
 }
 
 // sh.list[0, n) largest first (bitonic; n is padded to a power of two with zeros)
-__device__ __noinline__ void sort_list(Shared &sh, int n)
+template <int WARPS>
+__device__ __noinline__ void sort_list(Shared<WARPS> &sh, int n)
 {
     int m = 2;
     while (m < n) m *= 2;
-    for (int i = n + threadIdx.x; i < m; i += THREADS) sh.list[i] = 0;
+    for (int i = n + threadIdx.x; i < m; i += WARPS * 32) sh.list[i] = 0;
     for (int k = 2; k <= m; k *= 2)
         for (int j = k / 2; j > 0; j /= 2) {
             __syncthreads();
-            for (int p = threadIdx.x; p < m / 2; p += THREADS) {
+            for (int p = threadIdx.x; p < m / 2; p += WARPS * 32) {
                 const int i = 2 * p - (p & (j - 1)), q = i + j;
                 const u64 a = sh.list[i], b = sh.list[q];
                 if ((a < b) == ((i & k) == 0)) {
@@ -202,7 +209,8 @@ __device__ __forceinline__ float coarse_edge(int bin)
 }
 
 // The lanes' bins summed into sh.total.
-__device__ void sum_bins(Shared &sh)
+template <int WARPS>
+__device__ void sum_bins(Shared<WARPS> &sh)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();
@@ -220,25 +228,57 @@ __device__ void sum_bins(Shared &sh)
 }
 
 // The bin where `before` + the running sum first reaches `target` (or the last one with
-// anything in it); `before` becomes the sum up to it.
-__device__ int find_bin(const Shared &sh, u64 target, u64 &before)
+// anything in it); `before` becomes the sum up to it.  A lane for each bin.
+template <int WARPS>
+__device__ __forceinline__ int find_bin(const Shared<WARPS> &sh, u64 target, u64 &before)
 {
-    int at = 0;
-    u64 sum = before, upto = before;
-    for (int b = 0; b < BINS; ++b) {
-        const u64 x = sh.total[b];
-        if (x > 0) {
-            at = b;
-            upto = sum;
-            if (sum + x >= target) break;
-        }
-        sum += x;
+    const int lane = threadIdx.x & 31;
+    const u64 x = sh.total[lane];
+    u64 inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
     }
-    before = upto;
+    const uint32_t some = __ballot_sync(0xffffffffu, x > 0);
+    const uint32_t there = __ballot_sync(0xffffffffu, x > 0 && before + inc >= target);
+    const int at = there ? __ffs((int)there) - 1 : some ? 31 - __clz((int)some) : 0;
+    before += __shfl_sync(0xffffffffu, inc - x, at);
     return at;
 }
 
-__device__ __forceinline__ void clear_bins(Shared &sh)
+// For each of two predicates that are false up to some logit and true from there on: the
+// least logit up to the one of `top` for which it holds (NaN, which no logit compares
+// with: none).  Two warps search, 32 values a round.
+template <int WARPS, typename F>
+__device__ __forceinline__ float2 least_with(Shared<WARPS> &sh, uint32_t top, F f)
+{
+    __syncthreads();
+    const int which = threadIdx.x >> 5;
+    if (which < 2) {
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t a = KEY_NEG_INF, b = top;        // the answer lies in [a, b], or there is none
+#pragma unroll 1
+        while (a < b) {
+            const uint32_t step = (b - a) / 32 + 1, at = a + min(step * lane, b - a);
+            const uint32_t yes = __ballot_sync(0xffffffffu, f(which, unordered(at)));
+            if (yes == 0) {
+                a = __shfl_sync(0xffffffffu, at, 31) + 1;
+            } else {
+                const int k = __ffs((int)yes) - 1;
+                b = __shfl_sync(0xffffffffu, at, k);
+                a = k > 0 ? __shfl_sync(0xffffffffu, at, max(k - 1, 0)) + 1 : b;
+            }
+        }
+        if (lane == 0) sh.l[which] = f(which, unordered(b)) ? b : 0xffffffffu;
+    }
+    __syncthreads();
+    const uint32_t u = (uint32_t)sh.l[0], v = (uint32_t)sh.l[1];
+    return make_float2(unordered(u), unordered(v));               // 0xffffffff is a NaN's
+}
+
+template <int WARPS>
+__device__ __forceinline__ void clear_bins(Shared<WARPS> &sh)
 {
     __syncthreads();
     float *b = &sh.bins[threadIdx.x >> 5][0][threadIdx.x & 31];
@@ -257,11 +297,107 @@ __device__ __forceinline__ float exp2_approx(float x)
 // share of a 64-bit sum
 __device__ __forceinline__ u64 part_of(float f, u64 sum) { return (u64)((double)f * (double)sum); }
 
-template <typename E>
-__global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
+// What turns a logit into a weight.
+struct Scale {
+    float zref, floor, inv;
+    // gap to the largest logit: infinite for -inf, NaN and, where the largest is +inf, for
+    // all others; else finite, so that an infinite T makes it 0
+    __device__ __forceinline__ float gap(float x) const
+    {
+        return x > floor ? fminf(fmaxf(zref - x, 0.f), FLT_BIG) : INFINITY;
+    }
+    __device__ __forceinline__ float scaled(float g) const { return g * inv; }
+    __device__ __forceinline__ float weight(float g) const { return exp2_approx(-LOG2E * scaled(g)); }
+};
+
+// The threshold by bisection over the ordered values, for rows with too many candidates:
+// kept are the keys above thr, and those equal to it up to index cut.
+template <typename E, int WARPS>
+__device__ __noinline__ void bisect(Shared<WARPS> &sh, const E *z, int V, const Scale sc, uint32_t kmax, bool by_count, int k,
+                                    float tp, uint32_t &thr_out, int &cut_out)
 {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seg = (V + WARPS - 1) / WARPS, lo = min(V, warp * seg), hi = min(V, lo + seg);
+    uint32_t thr = 0;
+    int cut = V;
+    auto weight = [&](float g) { return sc.weight(g); };
+    auto gap = [&](float x) { return sc.gap(x); };
+    auto count_ge = [&](uint32_t key) {
+        int n = 0;
+        each(z, lo, hi, lane, 32, [&](int, float x) { n += ordered(x) >= key; });
+        return (int64_t)block_sum((u64)n, sh);
+    };
+    auto weight_ge = [&](uint32_t key) {
+        float s = 0.f;
+        each(z, lo, hi, lane, 32, [&](int, float x) { s += ordered(x) >= key ? weight(gap(x)) : 0.f; });
+        return block_sum(fixed(s), sh);
+    };
+    int64_t ties = V;                         // how many of those equal to thr stay
+    if (by_count) {
+        uint32_t a = 0, b = kmax;             // count_ge(a) >= k; the largest such key
+        while (a < b) {
+            const uint32_t mid = a + (b - a) / 2 + 1;
+            if (count_ge(mid) >= k) a = mid;
+            else b = mid - 1;
+        }
+        thr = a;
+        ties = k - count_ge(thr + 1);
+    }
+    if (tp < 1.f) {
+        const u64 wthr = fixed(weight(gap(unordered(thr))));
+        auto kept_ge = [&](uint32_t key) {    // weight of the kept with keys >= key
+            if (thr == 0) return weight_ge(key);
+            return key > thr ? weight_ge(key) : weight_ge(thr + 1) + (u64)ties * wthr;
+        };
+        const u64 target = part_of(fmaxf(tp, 0.f), kept_ge(0));
+        uint32_t a = thr, b = kmax;
+        while (a < b) {
+            const uint32_t mid = a + (b - a) / 2 + 1;
+            if (kept_ge(mid) >= target) a = mid;
+            else b = mid - 1;
+        }
+        const u64 above = kept_ge(a + 1), w = fixed(weight(gap(unordered(a))));
+        // equals i = 0, 1, ... stay while above + i w < target
+        int64_t stay = above >= target ? 0 : w > 0 ? (int64_t)((target - above + w - 1) / w) : V;
+        if (a == kmax && stay < 1) stay = 1;
+        if (a != thr || stay < ties) {
+            thr = a;
+            ties = stay;
+        }
+    }
+    if (ties < V) {
+        // where the equals that stay end, in index order: count them run by run
+        int n = 0;
+        for (int i = lo + lane; i < hi; i += 32) n += ordered(value(z, i)) == thr;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        __syncthreads();
+        if (lane == 0) sh.l[warp] = (u64)n;
+        if (tid == 0) sh.bl = (u64)V;
+        __syncthreads();
+        int64_t before = 0;
+        for (int w = 0; w < warp; ++w) before += (int64_t)sh.l[w];
+        if (before <= ties && before + n > ties) {           // the first equal that goes is here
+            for (int i0 = lo; i0 < hi; i0 += 32) {
+                const bool eq = i0 + lane < hi && ordered(value(z, i0 + lane)) == thr;
+                const uint32_t m = __ballot_sync(0xffffffffu, eq);
+                if (eq && before + __popc(m & ((1u << lane) - 1)) == ties) sh.bl = (u64)(i0 + lane);
+                before += __popc(m);
+            }
+        }
+        __syncthreads();
+        cut = (int)sh.bl;
+    }
+    thr_out = thr;
+    cut_out = cut;
+}
+
+template <typename E, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
+{
+    constexpr int THREADS = WARPS * 32;
     extern __shared__ __align__(16) uint8_t raw[];
-    Shared &sh = *reinterpret_cast<Shared *>(raw);
+    Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(raw);
     const int64_t row = blockIdx.x;
     const E *z = reinterpret_cast<const E *>(p.logits) + row * p.ld;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -288,12 +424,10 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
     const bool draw = T > 0.f, by_count = draw && k > 0 && k < V, by_weight = draw && !by_count && tp < 1.f;
     // 1 / T, kept above 0 so that an infinite gap stays infinite
     const float inv = draw ? fmaxf(1.f / T, 1.4e-45f) : 1.f;
-    // gap to the largest logit: infinite for -inf, NaN and, where the largest is +inf,
-    // for all others; else finite, so that an infinite T makes it 0
-    const float zref = fminf(zmax, FLT_BIG), floor = zmax < INFINITY ? -INFINITY : FLT_BIG;
-    auto gap = [&](float x) { return x > floor ? fminf(fmaxf(zref - x, 0.f), FLT_BIG) : INFINITY; };
-    auto scaled = [&](float g) { return g * inv; };
-    auto weight = [&](float g) { return exp2_approx(-LOG2E * scaled(g)); };
+    const Scale sc{fminf(zmax, FLT_BIG), zmax < INFINITY ? -INFINITY : FLT_BIG, inv};
+    auto gap = [&](float x) { return sc.gap(x); };
+    auto scaled = [&](float g) { return sc.scaled(g); };
+    auto weight = [&](float g) { return sc.weight(g); };
     float part = 0.f;                             // sum of e^(z - max)
     auto plain = [&](float g) { part += exp2_approx(-LOG2E * g); };
 
@@ -307,7 +441,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
         return key > thr || (key == thr && i < cut) ? (key == kmax || w >= mp ? w : 0.f) : 0.f;
     };
     bool slow = false;
-    float runs = 0.f;                             // kept weight of this warp's run, lane by lane
+    float runs = 0.f;                             // kept weight of this warp's run, lane by lane,
+    u64 extra = 0;                                // and what else belongs to the run
     bool have_runs = false;
 
     if (!draw) {
@@ -319,8 +454,8 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
         token = (int)~(uint32_t)block_max((uint32_t)~at, sh);
     } else if (by_count) {
         // a value that k of the threads' maxima reach: at least k logits do, and not many
-        // more.  2 k < THREADS keeps the expected number below 1.4 k (the measured rule:
-        // beyond it the candidates grow as the logarithm, and past CAP they are too many).
+        // more: below 1.4 k are expected while 2 k < THREADS.  Beyond, their number grows as the
+        // logarithm and soon passes CAP.
         uint32_t floor_key = 0;
         if (2 * k < THREADS) {
             const uint32_t own = ordered(top);
@@ -425,20 +560,36 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
         const int j = find_bin(sh, target, before);
         slow = j == BINS - 1;
         if (!slow) {
+            // from here on one comparison of the logit tells where it lies: the least logits
+            // whose gap falls into bin j or one before, and into one before
             const float from = coarse_edge(j), fine = BINS / (coarse_edge(j + 1) - from);
             auto sub = [&](float t) { return min(max((int)((t - from) * fine), 0), BINS - 1); };
+            const float2 in_j = least_with(sh, kmax, [&](int w, float x) { return coarse_bin(scaled(gap(x))) <= j - w; });
+            float in_lo = in_j.x, in_hi = in_j.y;
             clear_bins(sh);
             each(z, lo, hi, lane, 32, [&](int, float x) {
-                const float t = scaled(gap(x));
-                if (coarse_bin(t) == j) mine[32 * sub(t)] += exp2_approx(-LOG2E * t);
+                if (x >= in_lo && !(x >= in_hi)) {
+                    const float t = scaled(gap(x));
+                    mine[32 * sub(t)] += exp2_approx(-LOG2E * t);
+                }
             });
             sum_bins(sh);
             const int s = find_bin(sh, target, before);
+            const float2 in_s = least_with(sh, kmax, [&](int w, float x) {
+                const float t = scaled(gap(x));
+                return coarse_bin(t) < j || (coarse_bin(t) == j && sub(t) <= s - w);
+            });
+            in_lo = fmaxf(in_lo, in_s.x);
+            in_hi = fminf(in_hi, in_s.y);         // a NaN gives way to the other
             if (tid == 0) sh.n = 0;
             __syncthreads();
+            // what lies above the interval is kept: its weight, run by run, in the same pass
             each(z, lo, hi, lane, 32, [&](int i, float x) {
-                const float t = scaled(gap(x));
-                if (coarse_bin(t) == j && sub(t) == s) {
+                if (!(x >= in_lo)) return;
+                if (x >= in_hi) {
+                    const float w = weight(gap(x));
+                    runs += x == zmax || w >= mp ? w : 0.f;
+                } else {
                     const int at = atomicAdd(&sh.n, 1);          // any order: the list is sorted
                     if (at < CAP) sh.list[at] = (u64)ordered(x) << 32 | (uint32_t)~i;
                 }
@@ -470,96 +621,43 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
                 const u64 end = sh.list[max(n - 1, 0)];
                 thr = (uint32_t)(end >> 32);
                 cut = (int)~(uint32_t)end + (n > 0);
+                // the kept ones of the list join the runs they lie in
+                if (tid < WARPS) sh.l[tid] = 0;
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const int i = tid * PER + e;
+                    if (i < n && ((uint32_t)(sh.list[i] >> 32) == kmax || w[e] >= mp))
+                        atomicAdd(&sh.l[(int)~(uint32_t)sh.list[i] / seg], fixed(w[e]));
+                }
+                __syncthreads();
+                extra = sh.l[warp];
+                have_runs = true;
             }
         }
     } else {
-        each(z, lo, hi, lane, 32, [&](int i, float x) {
-            const float g = gap(x);
+        each(z, lo, hi, lane, 32, [&](int, float x) {
+            const float g = gap(x), w = weight(g);
             plain(g);
-            runs += kept(i, x, g);
+            runs += x == zmax || w >= mp ? w : 0.f;              // no threshold but min_p
         });
         have_runs = true;
     }
     const u64 all = block_sum(fixed(part), sh);
 
-    if (slow) {
-        // bisection over the ordered values
-        auto count_ge = [&](uint32_t key) {
-            int n = 0;
-            each(z, lo, hi, lane, 32, [&](int, float x) { n += ordered(x) >= key; });
-            return (int64_t)block_sum((u64)n, sh);
-        };
-        auto weight_ge = [&](uint32_t key) {
-            float s = 0.f;
-            each(z, lo, hi, lane, 32, [&](int, float x) { s += ordered(x) >= key ? weight(gap(x)) : 0.f; });
-            return block_sum(fixed(s), sh);
-        };
-        int64_t ties = V;                         // how many of those equal to thr stay
-        if (by_count) {
-            uint32_t a = 0, b = kmax;             // count_ge(a) >= k; the largest such key
-            while (a < b) {
-                const uint32_t mid = a + (b - a) / 2 + 1;
-                if (count_ge(mid) >= k) a = mid;
-                else b = mid - 1;
-            }
-            thr = a;
-            ties = k - count_ge(thr + 1);
-        }
-        if (tp < 1.f) {
-            const u64 wthr = fixed(weight(gap(unordered(thr))));
-            auto kept_ge = [&](uint32_t key) {    // weight of the kept with keys >= key
-                if (thr == 0) return weight_ge(key);
-                return key > thr ? weight_ge(key) : weight_ge(thr + 1) + (u64)ties * wthr;
-            };
-            const u64 target = part_of(fmaxf(tp, 0.f), kept_ge(0));
-            uint32_t a = thr, b = kmax;
-            while (a < b) {
-                const uint32_t mid = a + (b - a) / 2 + 1;
-                if (kept_ge(mid) >= target) a = mid;
-                else b = mid - 1;
-            }
-            const u64 above = kept_ge(a + 1), w = fixed(weight(gap(unordered(a))));
-            // equals i = 0, 1, ... stay while above + i w < target
-            int64_t stay = above >= target ? 0 : w > 0 ? (int64_t)((target - above + w - 1) / w) : V;
-            if (a == kmax && stay < 1) stay = 1;
-            if (a != thr || stay < ties) {
-                thr = a;
-                ties = stay;
-            }
-        }
-        if (ties < V) {
-            // where the equals that stay end, in index order: count them run by run
-            int n = 0;
-            for (int i = lo + lane; i < hi; i += 32) n += ordered(value(z, i)) == thr;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            __syncthreads();
-            if (lane == 0) sh.l[warp] = (u64)n;
-            if (tid == 0) sh.bl = (u64)V;
-            __syncthreads();
-            int64_t before = 0;
-            for (int w = 0; w < warp; ++w) before += (int64_t)sh.l[w];
-            if (before <= ties && before + n > ties) {           // the first equal that goes is here
-                for (int i0 = lo; i0 < hi; i0 += 32) {
-                    const bool eq = i0 + lane < hi && ordered(value(z, i0 + lane)) == thr;
-                    const uint32_t m = __ballot_sync(0xffffffffu, eq);
-                    if (eq && before + __popc(m & ((1u << lane) - 1)) == ties) sh.bl = (u64)(i0 + lane);
-                    before += __popc(m);
-                }
-            }
-            __syncthreads();
-            cut = (int)sh.bl;
-        }
-    }
+    if (slow) bisect<E, WARPS>(sh, z, V, sc, kmax, by_count, k, tp, thr, cut);
     if (token < 0) {
         // the draw over the row: the sums of the runs say which one holds the answer, and
         // the block goes through that one thread by thread
-        if (!have_runs) each(z, lo, hi, lane, 32, [&](int i, float x) { runs += kept(i, x, gap(x)); });
+        if (!have_runs) {
+            runs = 0.f;
+            each(z, lo, hi, lane, 32, [&](int i, float x) { runs += kept(i, x, gap(x)); });
+        }
         u64 ws = fixed(runs);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
         __syncthreads();
-        if (lane == 0) sh.l[warp] = ws;
+        if (lane == 0) sh.l[warp] = ws + extra;
         __syncthreads();
         u64 total = 0;
 #pragma unroll
@@ -603,12 +701,13 @@ __global__ void __launch_bounds__(THREADS, 2) sample_kernel(SampleParams p)
     }
 }
 
-template <typename E>
+template <typename E, int WARPS>
 caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
 {
-    auto kern = sample_kernel<E>;
-    if (prepare_kernel_smem((const void *)kern, (int)sizeof(Shared)) != CAAT_OK) return CAAT_ERR_CUDA;
-    launch_dependent(kern, dim3((unsigned)B), dim3(THREADS), sizeof(Shared), s, p);
+    auto kern = sample_kernel<E, WARPS>;
+    constexpr size_t smem = sizeof(Shared<WARPS>);
+    if (prepare_kernel_smem((const void *)kern, (int)smem) != CAAT_OK) return CAAT_ERR_CUDA;
+    launch_dependent(kern, dim3((unsigned)B), dim3(WARPS * 32), smem, s, p);
     if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("sample_tokens");
     return CAAT_OK;
@@ -621,7 +720,7 @@ caat_status launch_sample_tokens(int64_t B, int64_t V, caat_dtype dt, const void
                                  const float *min_p, int32_t *token, float *logprob, cudaStream_t s)
 {
     const SampleParams p{logits, ld, V, u, temperature, top_p, min_p, top_k, token, logprob};
-    return dt == CAAT_BF16 ? launch<__nv_bfloat16>(B, p, s) : launch<float>(B, p, s);
+    return dt == CAAT_BF16 ? launch<__nv_bfloat16, 16>(B, p, s) : launch<float, 16>(B, p, s);
 }
 
 }  // namespace caat
