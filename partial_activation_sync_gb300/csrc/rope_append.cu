@@ -37,23 +37,43 @@ struct AppendParams {
     PagedBatch pb;
 };
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[16], int at)
-{
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[at] = a.x, x[at + 1] = a.y, x[at + 2] = a.z, x[at + 3] = a.w;
-    x[at + 4] = b.x, x[at + 5] = b.y, x[at + 6] = b.z, x[at + 7] = b.w;
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[16], int at)
-{
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[at + 2 * i] = __uint_as_float(w[i] << 16);
-        x[at + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// The two runs of 8 values of a slot as they lie in memory.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 w[4];
+    __device__ __forceinline__ void load(const float *p, int d0, int d1)
+    {
+        w[0] = *reinterpret_cast<const float4 *>(p + d0), w[1] = *reinterpret_cast<const float4 *>(p + d0 + 4);
+        w[2] = *reinterpret_cast<const float4 *>(p + d1), w[3] = *reinterpret_cast<const float4 *>(p + d1 + 4);
     }
-}
+    __device__ __forceinline__ void get(float (&x)[16]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * i] = w[i].x, x[4 * i + 1] = w[i].y, x[4 * i + 2] = w[i].z, x[4 * i + 3] = w[i].w;
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 w[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int d0, int d1)
+    {
+        w[0] = *reinterpret_cast<const uint4 *>(p + d0), w[1] = *reinterpret_cast<const uint4 *>(p + d1);
+    }
+    __device__ __forceinline__ void get(float (&x)[16]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
+                x[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ void store8(float *p, const float (&x)[16], int at)
 {
@@ -153,7 +173,7 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int d0, int d1, const 
 template <typename E, bool INTER, bool WARP>
 __global__ void __launch_bounds__(WARP ? 128 : 1024) rope_append_kernel(AppendParams p, int slots_per_seq, int jobs_per, int job_chunks, int64_t teams)
 {
-    __shared__ float red[32];
+    __shared__ uint32_t red[2][32];
     const int team = WARP ? 32 : (int)blockDim.x;
     const int me = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
     const int64_t unit = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
@@ -211,19 +231,30 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) rope_append_kernel(AppendPa
         }
     }
     const int job_lo = chunk * jobs_per, job_hi = min(job_lo + jobs_per, p.heads + 2 * G);
+    const int held = lo - (j << p.kv.log2_page);
+    auto kind_of = [&](int job) { return job < p.heads ? 0 : job < p.heads + G ? 1 : 2; };
+    auto head_of = [&](int job) { return job < p.heads ? job : job < p.heads + G ? job - p.heads : job - p.heads - G; };
+    // threads without a row repeat row 0's loads (nothing they hold is written)
+    Raw<E> raw;
+    auto fetch = [&](int job) {
+        const int kind = kind_of(job), h = head_of(job);
+        const int64_t tt = live ? t : sq.t0 + (lo - sq.pos0);
+        raw.load(kind == 0 ? reinterpret_cast<const E *>(p.q) + tt * p.q_st + (h / p.group) * p.q_sk + (h % p.group) * p.q_sg
+                 : kind == 1 ? reinterpret_cast<const E *>(p.k) + tt * p.k_st + h * p.k_sh
+                             : reinterpret_cast<const E *>(p.v) + tt * p.v_st + h * p.v_sh,
+                 d0, d1);
+    };
+    fetch(job_lo);
+#pragma unroll 1
     for (int job = job_lo; job < job_hi; ++job) {
-        const int kind = job < p.heads ? 0 : job < p.heads + G ? 1 : 2;
-        const int h = kind == 0 ? job : (job - p.heads) % G;
-        const E *src = kind == 0 ? reinterpret_cast<const E *>(p.q) + t * p.q_st + (h / p.group) * p.q_sk +
-                                       (h % p.group) * p.q_sg
-                     : kind == 1 ? reinterpret_cast<const E *>(p.k) + t * p.k_st + h * p.k_sh
-                                 : reinterpret_cast<const E *>(p.v) + t * p.v_st + h * p.v_sh;
+        const int kind = kind_of(job), h = head_of(job);
+        float *scale = (kind == 1 ? p.kv.ks : p.kv.vs) + max(page, (int64_t)0) * p.kv.scale_stride + h;
+        // read by every thread before the barrier of the maximum, written by one behind it
+        const float s_old = kind != 0 && held > 0 ? *(volatile const float *)scale : 0.f;
         float x[16];
-        if (live) {
-            load8(src + d0, x, 0);
-            load8(src + d1, x, 8);
-            if (kind != 2 && turn) rotate16<INTER>(x, c, sn);
-        }
+        raw.get(x);
+        if (job + 1 < job_hi) fetch(job + 1);         // on its way while this one is worked on
+        if (kind != 2 && live && turn) rotate16<INTER>(x, c, sn);
         if (kind == 0) {
             if (live) {
                 E *o = reinterpret_cast<E *>(p.qo) + t * p.qo_st + h * p.qo_sh;
@@ -233,27 +264,19 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) rope_append_kernel(AppendPa
             continue;
         }
         if (page < 0) continue;                       // same for the whole team
-        float m = live ? amax16(x) : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!WARP) {
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-            __syncthreads();
-            m = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        }
-        float *scale = (kind == 1 ? p.kv.ks : p.kv.vs) + page * p.kv.scale_stride + h;
         uint8_t *codes = (kind == 1 ? p.kv.k : p.kv.v) + page * p.kv.page_stride + (int64_t)h * P * D;
-        const int held = lo - (j << p.kv.log2_page);
-        const float s_old = held > 0 ? *(volatile const float *)scale : 0.f;
-        const float s_new = fmaxf(s_old, pow2_scale(m));
+        // magnitudes are ordered as their bits are
+        uint32_t m = __reduce_max_sync(0xffffffffu, live ? __float_as_uint(amax16(x)) : 0u);
+        if (!WARP) {
+            uint32_t *r = red[job & 1];               // two in turn: one barrier a job
+            if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = m;
+            __syncthreads();
+            m = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < (blockDim.x >> 5) ? r[threadIdx.x & 31] : 0u);
+        }
+        const float s_new = fmaxf(s_old, pow2_scale(__uint_as_float(m)));
         if (held > 0 && s_new > s_old) rescale_rows(codes, held * D, s_old / s_new, me, team);
         if (live) store_codes(codes + (int64_t)(pos & (P - 1)) * D, d0, d1, x, 1.f / s_new);
-        // every thread of the team has read the old scale before it changes
         if (WARP) __syncwarp();
-        else __syncthreads();
         if (me == 0) *scale = s_new;
     }
 }
@@ -272,7 +295,13 @@ caat_status launch(const AppendParams &p, cudaStream_t s)
         launch_dependent(rope_append_kernel<E, INTER, true>, dim3((unsigned)blocks), dim3(128), 0, s, p, slots, 1, jobs, teams);
     } else {
         const int threads = (tokens * SL + 31) / 32 * 32;
-        const int jobs_per = 1, chunks = (jobs + jobs_per - 1) / jobs_per;
+        // Jobs in a row share the angles and the start-up; enough blocks stay to fill the SMs
+        // (4096 tokens, 32 + 2 x 32 heads of 128: 66 us with one job a block, 40 so, 48 with a third
+        // of the blocks; 48 short pieces, 16 + 2 x 16 heads of 48: 10.0, 8.9 so).
+        const int per_sm = 3072 / threads < 16 ? 3072 / threads : 16;
+        const int64_t all = (int64_t)p.pb.batch * slots * jobs, want = (int64_t)num_sms() * per_sm;
+        const int jobs_per = (int)(all / want < 1 ? 1 : all / want > 16 ? 16 : all / want);
+        const int chunks = (jobs + jobs_per - 1) / jobs_per;
         const int64_t blocks = (int64_t)p.pb.batch * slots * chunks;
         if (blocks > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
         launch_dependent(rope_append_kernel<E, INTER, false>, dim3((unsigned)blocks), dim3((unsigned)threads), 0, s, p, slots,

@@ -26,6 +26,10 @@ def _vector(x, n, dtype, name):
 
 
 def _stream(stream, like):
+    """The handle of `stream`, or of torch's current stream on the device of `like`."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None:
+        return raw(like.get_device())
     return _stream_ptr(stream, like).value or 0
 
 
@@ -133,30 +137,35 @@ def rope_append(q, k, v, cos, sin, cache, batch, interleaved=False, q_out=None, 
     of the token's position, in pairs (2i, 2i + 1) if interleaved, else (i, i + rot / 2);
     None: no rotation.  Returns the rotated queries [tokens, heads, dim] (``q_out``, which
     may be ``q``, allocated when None)."""
-    torch = _torch()
     T, H, q_st, q_sk, q_sg = _queries(q, cache)
-    kst = _strides(k, (T, cache.kv_heads, cache.dim), q.dtype, "k")
-    vst = _strides(v, (T, cache.kv_heads, cache.dim), q.dtype, "v")
-    dt = _dtype_code(q)
-    if (cos is None) != (sin is None):
-        raise ValueError("caat: cos and sin are given together")
-    positions, rot, cp, sp = 0, 0, None, None
-    if cos is not None:
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
-        for x, name in ((cos, "cos"), (sin, "sin")):
-            if x.shape != (positions, rot // 2) or x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
-                raise ValueError("caat: %s must be a dense CUDA tensor [positions, rot / 2] of dtype torch.float32" % name)
+    dtype, dim = q.dtype, cache.dim
+    kst, vst, shape = k.stride(), v.stride(), (T, cache.kv_heads, dim)
+    if (k.shape != shape or v.shape != shape or k.dtype != dtype or v.dtype != dtype or not k.is_cuda or not v.is_cuda
+            or kst[2] != 1 or vst[2] != 1):
+        raise ValueError("caat: k and v must be CUDA tensors %s of q's dtype, the last dimension dense" % list(shape))
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise ValueError("caat: cos and sin are given together")
+        positions, half, cp, sp = 0, 0, None, None
+    else:
+        positions, half = cos.shape
+        f32 = _torch().float32
+        if (sin.shape != cos.shape or cos.dtype != f32 or sin.dtype != f32 or not cos.is_cuda or not sin.is_cuda
+                or not cos.is_contiguous() or not sin.is_contiguous()):
+            raise ValueError("caat: cos and sin must be dense CUDA tensors [positions, rot / 2] of dtype torch.float32")
         cp, sp = cos.data_ptr(), sin.data_ptr()
     if q_out is None:
-        q_out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
-    ost = _strides(q_out, (T, H, cache.dim), q.dtype, "q_out")
+        q_out = _torch().empty((T, H, dim), dtype=dtype, device=q.device)
+        o_t, o_h = H * dim, dim
+    else:
+        o_t, o_h, _ = _strides(q_out, (T, H, dim), dtype, "q_out")
     batch._c.tokens = T
     st = _lib.load().caat_rope_append(
-        cache._ref, batch._ref, H, dt, q.data_ptr(), q_st, q_sk, q_sg,
-        k.data_ptr(), kst[0], kst[1], v.data_ptr(), vst[0], vst[1],
-        cp, sp, positions, rot, 1 if interleaved else 0, q_out.data_ptr(), ost[0], ost[1],
+        cache._ref, batch._ref, H, _dtype_code(q), q.data_ptr(), q_st, q_sk, q_sg, k.data_ptr(), kst[0], kst[1],
+        v.data_ptr(), vst[0], vst[1], cp, sp, positions, 2 * half, 1 if interleaved else 0, q_out.data_ptr(), o_t, o_h,
         _stream(stream, q))
-    _check(st, "caat_rope_append")
+    if st:
+        _check(st, "caat_rope_append")
     return q_out
 
 
@@ -167,18 +176,20 @@ def paged_attention(q, cache, batch, softmax_scale=None, window=0, sinks=0, out=
     cached keys j <= p; with window > 0 only j > p - window and j < sinks (the first tokens
     stay visible).  softmax_scale: 1 / sqrt(dim) when None.  Returns [tokens, heads, dim]
     of q's dtype (``out``, allocated when None); a query that sees nothing gives zeros."""
-    torch = _torch()
     T, H, q_st, q_sk, q_sg = _queries(q, cache)
-    dt = _dtype_code(q)
+    dim = cache.dim
     if out is None:
-        out = torch.empty((T, H, cache.dim), dtype=q.dtype, device=q.device)
-    ost = _strides(out, (T, H, cache.dim), q.dtype, "out")
+        out = _torch().empty((T, H, dim), dtype=q.dtype, device=q.device)
+        o_t, o_h = H * dim, dim
+    else:
+        o_t, o_h, _ = _strides(out, (T, H, dim), q.dtype, "out")
     batch._c.tokens = T
     st = _lib.load().caat_paged_attention(
-        cache._ref, batch._ref, H, dt, q.data_ptr(), q_st, q_sk, q_sg,
-        cache.dim ** -0.5 if softmax_scale is None else float(softmax_scale), int(window), int(sinks),
-        out.data_ptr(), ost[0], ost[1], _stream(stream, q))
-    _check(st, "caat_paged_attention")
+        cache._ref, batch._ref, H, _dtype_code(q), q.data_ptr(), q_st, q_sk, q_sg,
+        dim ** -0.5 if softmax_scale is None else softmax_scale, window, sinks, out.data_ptr(), o_t, o_h,
+        _stream(stream, q))
+    if st:
+        _check(st, "caat_paged_attention")
     return out
 
 
@@ -201,9 +212,10 @@ def sample_tokens(logits, u, temperature, top_k, top_p, min_p, tokens=None, logp
     if logprobs is None:
         logprobs = torch.empty(B, dtype=f32, device=logits.device)
     st = _lib.load().caat_sample_tokens(
-        B, V, _dtype_code(logits), logits.data_ptr(), logits.stride(0) if B > 1 else V,
-        _vector(u, B, f32, "u"), _vector(temperature, B, f32, "temperature"), _vector(top_k, B, i32, "top_k"),
-        _vector(top_p, B, f32, "top_p"), _vector(min_p, B, f32, "min_p"), _vector(tokens, B, i32, "tokens"),
-        _vector(logprobs, B, f32, "logprobs"), _stream(stream, logits))
-    _check(st, "caat_sample_tokens")
+        B, V, _dtype_code(logits), logits.data_ptr(), logits.stride(0) if B > 1 else V, _vector(u, B, f32, "u"),
+        _vector(temperature, B, f32, "temperature"), _vector(top_k, B, i32, "top_k"), _vector(top_p, B, f32, "top_p"),
+        _vector(min_p, B, f32, "min_p"), _vector(tokens, B, i32, "tokens"), _vector(logprobs, B, f32, "logprobs"),
+        _stream(stream, logits))
+    if st:
+        _check(st, "caat_sample_tokens")
     return tokens, logprobs
