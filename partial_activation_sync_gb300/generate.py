@@ -1,0 +1,159 @@
+"""Generation with a CAAT-Net block stack: prompts and single tokens over a paged 8-bit
+key-value cache, the t tensor-parallel ranks emulated on one GPU.
+
+Every product of a block runs in the library's column- and row-parallel layers with the
+partial channel-reduce, as in training (``caatnet.Block``); between them the rotary
+append, the paged attention and, after the last block, the sampling of ``serving`` take
+the place of the training stack's attention over whole sequences.  Norms, GELU, residual
+adds, embedding and LM head are PyTorch ops, as there.
+
+    python -m partial_activation_sync_gb300.generate --batch 4 --prompt 100 --new 64
+"""
+import argparse
+import time
+
+import torch
+import torch.nn.functional as F
+
+from . import (PagedBatch, PagedKVCache, colpar_linear_fwd, paged_attention, rope_append, rowpar_linear_fwd,
+               sample_tokens)
+from .caatnet import CAATNet, rope_tables
+
+
+class Generator:
+    """Serves one batch of sequences with the weights of ``model`` (a CAATNet).
+
+    max_len: most tokens a sequence may reach; page: tokens of a cache page.  Each
+    sequence owns ceil(max_len / page) pages of every layer's cache."""
+
+    def __init__(self, model, batch, max_len, page=64):
+        self.model, self.t, self.page, self.max_len = model, model.t, page, max_len
+        h, heads = model.h, model.heads
+        self.hd = hd = h // heads
+        dev, self.dtype = model.emb.device, model.emb.dtype
+        # The training layout of a rank's QKV columns is [3, heads, hd].  With [heads, 3, hd] the
+        # queries, keys and values of a projection are strided views [tokens, heads, hd] across
+        # all ranks: laid out once here.
+        t, hpr = model.t, heads // model.t
+        self.wqkv = [b.wqkv.detach().view(h, t, 3, hpr, hd).permute(0, 1, 3, 2, 4).reshape(h, 3 * h).contiguous()
+                     for b in model.blocks]
+        self.cos, self.sin = rope_tables(max_len, hd, dev, torch.float32)
+        width = -(-max_len // page)
+        self.caches = [PagedKVCache.empty(batch * width, heads, page, hd, device=dev) for _ in model.blocks]
+        self.page_table = torch.arange(batch * width, dtype=torch.int32, device=dev).view(batch, width)
+        self.kv_len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.last = torch.zeros(batch, dtype=torch.int32, device=dev)       # last token of each sequence
+        self.one_each = torch.arange(batch + 1, dtype=torch.int32, device=dev)
+        self.graph = None
+
+    def _colpar(self, a, w):
+        """Column-parallel product of few or many tokens: its tensor-core kernel takes 128 and
+        more, so fewer are padded."""
+        N = a.shape[1]
+        if N < 128:
+            a = F.pad(a, (0, 0, 0, 128 - N))
+        return colpar_linear_fwd(a, w, self.t)[:N]
+
+    def _stack(self, tokens, step):
+        """Residual streams [t, N, h] after the blocks, for packed tokens [N]."""
+        m, t = self.model, self.t
+        N, sel = tokens.shape[0], m.sel()
+        x = F.embedding(tokens, m.emb).unsqueeze(0).expand(t, N, m.h).contiguous()
+        for blk, wqkv, cache in zip(m.blocks, self.wqkv, self.caches):
+            z = self._colpar(blk.ln1(x), wqkv).view(N, m.heads, 3, self.hd)
+            q = rope_append(z[:, :, 0], z[:, :, 1], z[:, :, 2], self.cos, self.sin, cache, step, interleaved=True)
+            o = paged_attention(q, cache, step).view(N, m.h)
+            x = x + torch.stack(rowpar_linear_fwd(o, blk.wo.t(), t, sel))
+            u = F.gelu(self._colpar(blk.ln2(x), blk.w1))
+            x = x + torch.stack(rowpar_linear_fwd(u, blk.w2.t(), t, sel))
+        return x
+
+    def _logits(self, x):
+        return self.model.ln_f(x.mean(dim=0)) @ self.model.emb.t()
+
+    @torch.no_grad()
+    def prefill(self, prompts):
+        """Takes the sequences' first (or next) tokens, a list of 1-D integer tensors; returns
+        the logits [batch, vocab] behind each one's last token."""
+        n = [int(p.shape[0]) for p in prompts]
+        tokens = torch.cat([p.to(self.kv_len.device) for p in prompts])
+        start = torch.tensor([0] + n).cumsum(0).to(torch.int32).to(tokens.device)
+        self.kv_len += start[1:] - start[:-1]
+        x = self._stack(tokens, PagedBatch(self.page_table, start, self.kv_len, max(n)))
+        return self._logits(x[:, (start[1:] - 1).long()])
+
+    @torch.no_grad()
+    def decode(self, tokens):
+        """One more token of each sequence, int [batch]; returns the logits [batch, vocab]."""
+        self.kv_len += 1
+        return self._logits(self._stack(tokens, PagedBatch(self.page_table, self.one_each, self.kv_len, 1)))
+
+    @torch.no_grad()
+    def generate(self, prompts, new, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+        """Samples `new` tokens for each prompt from the uniform numbers u [new, batch].
+        Returns int32 [batch, new].  The single-token steps run as one CUDA graph, captured at
+        the first call and replayed with new numbers in the same buffers."""
+        B, dev = self.kv_len.shape[0], self.kv_len.device
+        full = lambda v, dt: torch.full((B,), v, dtype=dt, device=dev)  # noqa: E731
+        how = (full(float(temperature), torch.float32), full(int(top_k), torch.int32), full(float(top_p), torch.float32),
+               full(float(min_p), torch.float32))
+        out = torch.empty(B, new, dtype=torch.int32, device=dev)
+        out[:, 0], _ = sample_tokens(self.prefill(prompts), u[0].contiguous(), *how)
+        if new == 1:
+            return out
+        if self.graph is None:
+            self.u, self.how = torch.empty(B, device=dev), [x.clone() for x in how]
+
+            def step():
+                tokens, _ = sample_tokens(self.decode(self.last), self.u, *self.how)
+                self.last.copy_(tokens)
+
+            # a run before the capture sets the kernels up; its token and its place in the cache
+            # are taken back
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                self.last.zero_()
+                self.u.zero_()
+                step()
+                self.kv_len -= 1
+            torch.cuda.current_stream().wait_stream(side)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                step()
+        for mine, x in zip(self.how, how):
+            mine.copy_(x)
+        self.last.copy_(out[:, 0])
+        for i in range(1, new):
+            self.u.copy_(u[i])
+            self.graph.replay()
+            out[:, i] = self.last
+        return out
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
+    ap.add_argument("--batch", type=int, default=4)
+    ap.add_argument("--prompt", type=int, default=100, help="tokens of a prompt")
+    ap.add_argument("--new", type=int, default=64, help="tokens to generate")
+    ap.add_argument("--seed", type=int, default=0)
+    a = ap.parse_args()
+    torch.manual_seed(a.seed)
+    model = CAATNet().cuda().bfloat16()                  # the 130M stack, random weights
+    gen = Generator(model, a.batch, a.prompt + a.new)
+    prompts = [torch.randint(0, model.emb.shape[0], (a.prompt,)) for _ in range(a.batch)]
+    u = torch.rand(a.new, a.batch, device="cuda")
+    for run in range(2):                                 # the second one replays the captured step
+        gen.kv_len.zero_()
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        out = gen.generate(prompts, a.new, u, temperature=0.8, top_k=50, top_p=0.95)
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    print("%d sequences, prompt %d, %d new tokens each: %.1f ms, %.0f tokens/s" %
+          (a.batch, a.prompt, a.new, dt * 1e3, a.batch * a.new / dt))
+    print("first tokens:", out[:, :8].tolist())
+
+
+if __name__ == "__main__":
+    main()
