@@ -428,8 +428,17 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
     auto gap = [&](float x) { return sc.gap(x); };
     auto scaled = [&](float g) { return sc.scaled(g); };
     auto weight = [&](float g) { return sc.weight(g); };
-    float part = 0.f;                             // sum of e^(z - max)
-    auto plain = [&](float g) { part += exp2_approx(-LOG2E * g); };
+    // Sum of e^(z - max), the maxima counted apart: the log probability of a likely token is
+    // small, and a rounding of 1 + rest would be large beside it.  What -g log2(e) loses in
+    // rounding, and log2(e) itself, is put back to first order.
+    float part = 0.f;
+    int equal = 0;
+    auto plain = [&](float g) {
+        const float h = fminf(g, 200.f), y = -LOG2E * h, w = exp2_approx(y);      // 0 at 200 and beyond
+        const float e = fmaf(-h, LOG2E, -y) - h * 1.9259630e-8f;
+        equal += g == 0.f;
+        part += g > 0.f ? fmaf(w, e * 0.6931472f, w) : 0.f;
+    };
 
     int token = -1;
     // kept: keys above thr, and those equal to it up to index cut; weights from mp on
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
         });
         have_runs = true;
     }
-    const u64 all = block_sum(fixed(part), sh);
+    const u64 rest = block_sum(fixed(part) + ((u64)equal << 40), sh) - (1ull << 40);      // beyond the first 1
 
     if (slow) bisect<E, WARPS>(sh, z, V, sc, kmax, by_count, k, tp, thr, cut);
     if (token < 0) {
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
     if (tid == 0) {
         const float x = value(z, token);
         p.token[row] = token;
-        p.logprob[row] = (x == zmax ? 0.f : x - zmax) - logf((float)all * (1.f / ONE));
+        p.logprob[row] = (x == zmax ? 0.f : x - zmax) - log1pf((float)rest * (1.f / ONE));
     }
 }
 

@@ -468,3 +468,15 @@ def test_calls_follow_their_stream_and_replay_in_a_graph():
     want = step()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert caat.device_status() == 0
+
+
+def test_sample_logprob_of_a_likely_token():
+    # one token far above the rest: its log probability is -log(1 + rest), and the rest must
+    # not be lost beside the 1.  Each weight is good to about 2^-21, their fp32 sums (128 terms
+    # a thread) to 2^-20, and so is the logarithm, relatively.
+    for V, gap in ((1000, 12.0), (32000, 16.0), (32000, 20.0), (500, 30.0)):
+        z = torch.randn(4, V, generator=_gen(V)).float()
+        z[:, 77] = gap
+        tok, lp = _sample(z, 0.5, 0.0, 0, 1.0, 0.0)
+        want = torch.log_softmax(z.double(), -1)[:, 77].numpy()
+        assert (tok == 77).all() and (np.abs(lp - want) <= 2.0 ** -18 * np.abs(want)).all(), (V, gap, lp, want)
