@@ -137,6 +137,30 @@ __device__ __forceinline__ u64 block_sum(u64 x, Shared<WARPS> &sh)
     return x;
 }
 
+// sum over the block of weights that may all be below 2^-40, and of small counts (to 2^24,
+// exact), less one: in fp32, always in the same order
+template <int WARPS>
+__device__ __forceinline__ float block_rest(float part, int count, Shared<WARPS> &sh)
+{
+    float n = (float)count;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        part += __shfl_xor_sync(0xffffffffu, part, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh.l[threadIdx.x >> 5] = (u64)__float_as_uint(n) << 32 | __float_as_uint(part);
+    __syncthreads();
+    const u64 both = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
+    part = __uint_as_float((uint32_t)both), n = __uint_as_float((uint32_t)(both >> 32));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        part += __shfl_xor_sync(0xffffffffu, part, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    return n - 1.f + part;
+}
+
 // sum of the values of the threads below this one, and of all
 template <int WARPS>
 __device__ __forceinline__ u64 block_scan(u64 x, Shared<WARPS> &sh, u64 &all)
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
         });
         have_runs = true;
     }
-    const u64 rest = block_sum(fixed(part) + ((u64)equal << 40), sh) - (1ull << 40);      // beyond the first 1
+    const float rest = block_rest(part, equal, sh);               // beyond the first maximum's 1
 
     if (slow) bisect<E, WARPS>(sh, z, V, sc, kmax, by_count, k, tp, thr, cut);
     if (token < 0) {
@@ -706,7 +730,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
     if (tid == 0) {
         const float x = value(z, token);
         p.token[row] = token;
-        p.logprob[row] = (x == zmax ? 0.f : x - zmax) - log1pf((float)rest * (1.f / ONE));
+        p.logprob[row] = (x == zmax ? 0.f : x - zmax) - log1pf(rest);
     }
 }
 

@@ -478,5 +478,8 @@ def test_sample_logprob_of_a_likely_token():
         z = torch.randn(4, V, generator=_gen(V)).float()
         z[:, 77] = gap
         tok, lp = _sample(z, 0.5, 0.0, 0, 1.0, 0.0)
-        want = torch.log_softmax(z.double(), -1)[:, 77].numpy()
+        # (a 64-bit sum that holds the 1 too is off by 2^-53 a term: 1e-5 of a rest of 7e-11)
+        rest = (z.double() - gap).exp()
+        rest[:, 77] = 0.0
+        want = -torch.log1p(rest.sum(-1)).numpy()
         assert (tok == 77).all() and (np.abs(lp - want) <= 2.0 ** -18 * np.abs(want)).all(), (V, gap, lp, want)
