@@ -3,6 +3,8 @@
 // indices, and the e4m3 conversions.
 #pragma once
 
+#include <climits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,6 +54,32 @@ __device__ __forceinline__ Seq load_seq(const PagedBatch &pb, int page, int b, i
         s.n = 0;
     }
     return s;
+}
+
+constexpr int MAX_RANKED = 1024;     // sequences that by_length takes
+
+// The sequence with the b-th most cached tokens (equals by number).  Blocks that do not all
+// run at once start in order, and a long sequence left for the end keeps the others waiting.
+// For all threads of a block; shared: MAX_RANKED + 1 words, 16-byte aligned, free again after.
+__device__ __forceinline__ int by_length(const PagedBatch &pb, int b, int *shared)
+{
+    int *mine = shared + MAX_RANKED;
+    for (int i = threadIdx.x; i < MAX_RANKED; i += blockDim.x) shared[i] = i < pb.batch ? __ldg(pb.kv_len + i) : INT_MIN;
+    __syncthreads();
+    for (int i = threadIdx.x; i < pb.batch; i += blockDim.x) {
+        const int n = shared[i];
+        int before = 0;
+        for (int j = 0; j < pb.batch; j += 4) {
+            const int4 o = *reinterpret_cast<const int4 *>(shared + j);
+            before += (o.x > n || (o.x == n && j < i)) + (o.y > n || (o.y == n && j + 1 < i)) +
+                      (o.z > n || (o.z == n && j + 2 < i)) + (o.w > n || (o.w == n && j + 3 < i));
+        }
+        if (before == b) *mine = i;
+    }
+    __syncthreads();
+    b = *mine;
+    __syncthreads();
+    return b;
 }
 
 // a page number of the table, or -1 (recorded in *err) when the cache has no such page

@@ -4,7 +4,7 @@
 // A block holds two tiles of 128 query rows (row = new token x query head of the cached
 // head) and goes through the cached keys 128 at a time:
 //     S = Q K^T            tcgen05, operands in shared memory, S in TMEM
-//     P = 2^(c S - m)      one thread a row, S from TMEM, P (f16) over S's place in TMEM
+//     P = 2^(c S - m)      two threads a row, S from TMEM, P (f16) over S's place in TMEM
 //     O += P V             tcgen05, P from TMEM, O in TMEM
 // with the running row maximum m and sum in registers.  While one tile's softmax runs,
 // the tensor cores work for the other.  m moves only when a row's maximum grew by more
@@ -66,7 +66,6 @@ struct Ctl {
     uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full[2], p_full[2];
     uint32_t tmem;
     int abort, v_nan;
-    float ref_k, ref_v;
     float part[2][8];
     float up[2 * TILE], top[2][2][2 * TILE];     // [parity][half][row]
 };
@@ -246,17 +245,22 @@ __global__ void __launch_bounds__(THREADS, 1) paged_attn_tile_kernel(const __gri
     volatile int *abort = &ctl->abort;
     const int P = p.kv.page, D = p.kv.dim;
 
+    // The last rows of a prompt see the most keys: their chunks start first, and of several
+    // sequences the longest (four pieces of 257 to 1025 tokens, 32 heads of 128 over 8, behind
+    // 3001 to 15001 cached ones: 501 us; all last chunks first, 592).
+    const int split = (int)(blockIdx.x % p.splits);
+    int64_t unit = blockIdx.x / p.splits;
+    const int head = (int)(unit % p.kv.kv_heads);
+    unit /= p.kv.kv_heads;
+    const int chunk = p.chunks - 1 - (int)(unit % p.chunks);
+    int seq = (int)(unit / p.chunks);
+    if (p.pb.batch > 1 && p.pb.batch <= MAX_RANKED) seq = by_length(p.pb, seq, reinterpret_cast<int *>(bufs));
+
     // Which rows and keys are this block's: worked out by one thread, read from shared
     // memory by each role as far as it needs them (registers are what the roles lack).
     if (tid == 0) {
         Work w;
-        const int split = (int)(blockIdx.x % p.splits);
-        int64_t unit = blockIdx.x / p.splits;
-        // the last rows of a prompt see the most keys: their chunks start first
-        const int64_t per_chunk = (int64_t)p.pb.batch * p.kv.kv_heads;
-        const int chunk = p.chunks - 1 - (int)(unit / per_chunk);
-        unit %= per_chunk;
-        w.h = (int)(unit % p.kv.kv_heads), w.b = (int)(unit / p.kv.kv_heads);
+        w.h = head, w.b = seq;
         const Seq sq = load_seq(p.pb, P, w.b, p.err);
         w.t0 = sq.t0, w.pos0 = sq.pos0;
         w.row0 = chunk * 2 * TILE;

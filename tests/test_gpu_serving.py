@@ -117,6 +117,23 @@ def test_attention_long_split_over_blocks():
     _attention([70, 3, 200], [2500, 40, 200], 2, 1, 96, 32, "bf16", seed=9)
 
 
+@pytest.mark.parametrize("batch,kv_heads,dim,dtype", [(161, 2, 64, "bf16"), (330, 1, 128, "f32"), (1027, 1, 16, "bf16")])
+def test_attention_of_more_blocks_than_run_at_once(batch, kv_heads, dim, dtype):
+    # sequences start in the order of their lengths: odd batches, equal lengths, empty ones,
+    # and a batch above the number that is put in order
+    kv = [(37 * b) % 61 * (1 + b % 3) for b in range(batch)]
+    new = [min(n, 1 + (b % 11 == 0)) for b, n in enumerate(kv)]
+    _attention(new, kv, 2 * kv_heads, kv_heads, dim, 16, dtype, seed=batch)
+
+
+@pytest.mark.parametrize("batch,window", [(3, 0), (37, 0), (1027, 20)])
+def test_attention_many_pieces(batch, window):
+    # the tile kernel over sequences of different lengths, some without new tokens
+    new = [[33, 0, 70, 2][b % 4] if batch < 100 or b % 257 == 0 else b % 2 for b in range(batch)]
+    kv = [n + (53 * b) % 207 for b, n in enumerate(new)]
+    _attention(new, kv, 12, 3, 64, 32, "bf16", window=window, seed=batch)
+
+
 def test_attention_rows_that_see_nothing_are_zero():
     table, start, length, pages = ref.make_tables([1, 1, 3], [0, 5, 2], 16, width=2)
     k, v, ks, vs = _cache(0, pages, 2, 16, 64)
