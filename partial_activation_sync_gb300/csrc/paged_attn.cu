@@ -23,6 +23,10 @@
 // the same speed.  fp32 queries are split into two f16 (22 bits), as are the weights,
 // at twice the products.  The scales of a page multiply the scores after the product
 // (keys) and the weights before it (values), in fp32.
+//
+// Measured (device time), bf16: one token behind 4096 keys, 32 heads of 128: 11.9 us, mostly
+// launch, page lookups and the join; 128 ragged sequences of up to 4096, 4 cached heads of 64:
+// 33.0 us, 4.2 TB/s, bound by the instructions of a step (widening, scales, exponentials).
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 

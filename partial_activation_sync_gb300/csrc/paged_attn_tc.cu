@@ -20,6 +20,11 @@
 // sees (2^0 .. 2^-24 in f16, exact while a code times that ratio is at least 2^-24).  So
 // scores and outputs carry one factor a row and no scale inside the loop.
 //
+// Measured (device time): a prompt of 4096, 32 heads of 128: 161 us, 851 TFLOP/s; pieces of
+// 257 to 1025 tokens behind 3001 to 15001, 32 heads over 8: 501 us, 1090 TFLOP/s.  A step of
+// 128 keys takes some 4000 cycles a pair of tiles: the softmax chain (TMEM reads,
+// exponentials, weights back) about 3000, the products 1040 to 1300 a tile.
+//
 // When the blocks are fewer than the SMs, a cluster splits the keys of a row chunk and
 // joins its shares over distributed shared memory.
 #include <type_traits>
