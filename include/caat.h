@@ -44,7 +44,8 @@
  *    stages whatever the tile width; single CTAs only), CAAT_BWD_PAIR=0 (the
  *    backward GEMMs on single CTAs instead of CTA pairs), CAAT_PDL=0 (the
  *    forward kernels, the backward GEMMs, the sum of the gradient's S channels
- *    and the standalone reduce launched plainly instead of as programmatic
+ *    the standalone reduce, the rotary append, the attention of few rows and the
+ *    sampling launched plainly instead of as programmatic
  *    dependents of the previous launch in the stream, whose blocks may then start
  *    while that launch finishes; they wait for it before they touch memory).
  *  - CAAT_CHECK_SEL=1 (a debug switch) checks every index list of S: the list is

@@ -25,11 +25,13 @@
 // exact in any order, and the chip's fp64 rate is too low for the short chains between
 // the passes.
 //
-// One block for a row, each warp on one run of it, so that the sums of the runs say
-// where the drawn token lies.  The passes after the first find the row in L2 or L1.
-// Bound by the instructions of those passes for large vocabularies and by the latency
-// of the chain for few rows: 17 us for one row of 32000, 38 us for 64 of them (fp32), 144 us
-// for 256 rows of 131071 (bf16), on the device.
+// A row is shared by the blocks of a cluster, each warp on one run of it, so that the sums of
+// the runs say where the drawn token lies.  The blocks exchange the maximum and the bins'
+// sums over distributed shared memory; then the first takes the others' candidates and
+// runs' weights and ends the work alone.  The passes after the first find the row in L2 or
+// L1.  Bound by the instructions of those passes for large batches and by the latency of the
+// chain for few rows (device time): 14.0 us for one row of 32000 (bf16), 26.8 us for 64 of
+// them (fp32), 114 us for 256 rows of 131071 (bf16).
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -37,6 +39,7 @@ namespace caat {
 namespace {
 
 constexpr int BINS = 32;
+constexpr int MAX_SPLITS = 8;                   // blocks that share a row
 constexpr int CAP = 2048;                       // values that are sorted in shared memory
 constexpr float FLT_BIG = 3.402823466e38f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -118,6 +121,9 @@ struct Shared {
     u64 l[WARPS];
     u64 bl;
     int n;
+    // from the blocks of the row's cluster
+    u64 word[2][MAX_SPLITS], totals[2][MAX_SPLITS][BINS];
+    u64 runs[MAX_SPLITS * WARPS], rests[MAX_SPLITS], best[MAX_SPLITS];
 };
 
 constexpr float ONE = 1099511627776.f;          // 2^40: a weight of 1
@@ -138,10 +144,12 @@ __device__ __forceinline__ u64 block_sum(u64 x, Shared<WARPS> &sh)
     return x;
 }
 
-// sum over the block of weights that may all be below 2^-40, and of small counts (to 2^24,
-// exact), less one: in fp32, always in the same order
+// sums over the block of weights that may all be below 2^-40, and of small counts (to 2^24,
+// exact), in fp32 and always in the same order; packed
+__device__ __forceinline__ u64 pack_rest(float part, float n) { return (u64)__float_as_uint(n) << 32 | __float_as_uint(part); }
+
 template <int WARPS>
-__device__ __forceinline__ float block_rest(float part, int count, Shared<WARPS> &sh)
+__device__ __forceinline__ u64 block_rest(float part, int count, Shared<WARPS> &sh)
 {
     float n = (float)count;
 #pragma unroll
@@ -150,7 +158,7 @@ __device__ __forceinline__ float block_rest(float part, int count, Shared<WARPS>
         n += __shfl_xor_sync(0xffffffffu, n, o);
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.l[threadIdx.x >> 5] = (u64)__float_as_uint(n) << 32 | __float_as_uint(part);
+    if ((threadIdx.x & 31) == 0) sh.l[threadIdx.x >> 5] = pack_rest(part, n);
     __syncthreads();
     const u64 both = (threadIdx.x & 31) < WARPS ? sh.l[threadIdx.x & 31] : 0;
     part = __uint_as_float((uint32_t)both), n = __uint_as_float((uint32_t)(both >> 32));
@@ -159,7 +167,22 @@ __device__ __forceinline__ float block_rest(float part, int count, Shared<WARPS>
         part += __shfl_xor_sync(0xffffffffu, part, o);
         n += __shfl_xor_sync(0xffffffffu, n, o);
     }
-    return n - 1.f + part;
+    return pack_rest(part, n);
+}
+
+// a word of shared memory of this block (its address there) in the cluster's block `rank`
+__device__ __forceinline__ void st_peer(const u64 *own, int rank, u64 x)
+{
+    asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(tc::map_to_cta(tc::smem_u32(own), (uint32_t)rank)), "l"(x) : "memory");
+}
+__device__ __forceinline__ int add_peer(const int *own, int rank, int x)
+{
+    int r;
+    asm volatile("atom.shared::cluster.add.s32 %0, [%1], %2;"
+                 : "=r"(r)
+                 : "r"(tc::map_to_cta(tc::smem_u32(own), (uint32_t)rank)), "r"(x)
+                 : "memory");
+    return r;
 }
 
 // sum of the values of the threads below this one, and of all
@@ -201,15 +224,43 @@ __device__ __forceinline__ u64 block_max(u64 x, Shared<WARPS> &sh)
     return x;
 }
 
-// sh.list[0, n) largest first (bitonic; n is padded to a power of two with zeros)
+// the largest over the row's blocks; `use` numbers the calls of a row
+template <int WARPS>
+__device__ __forceinline__ u64 row_max(u64 x, Shared<WARPS> &sh, int splits, int rank, int use)
+{
+    x = block_max(x, sh);
+    if (splits == 1) return x;
+    if (threadIdx.x < splits) st_peer(&sh.word[use][rank], threadIdx.x, x);
+    tc::cluster_sync();
+    for (int i = 0; i < splits; ++i) x = max(x, sh.word[use][i]);
+    return x;
+}
+
+// The exchange of two values j apart within a warp, in runs of k that are to be falling
+// where (i & k) == 0.
+__device__ __forceinline__ u64 exchange(u64 x, int i, int k, int j)
+{
+    const u64 y = __shfl_xor_sync(0xffffffffu, x, j);
+    return ((i & k) == 0) == ((i & j) == 0) ? max(x, y) : min(x, y);
+}
+
+// sh.list[0, n) largest first (bitonic; n is padded to a power of two with zeros).  Distances
+// below a warp's 32 are exchanged in registers: 512 values take 10 barriers more than the
+// passes through them, not 45.
 template <int WARPS>
 __device__ __noinline__ void sort_list(Shared<WARPS> &sh, int n)
 {
-    int m = 2;
+    int m = 32;
     while (m < n) m *= 2;
-    for (int i = n + threadIdx.x; i < m; i += WARPS * 32) sh.list[i] = 0;
-    for (int k = 2; k <= m; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += WARPS * 32) {
+        u64 x = i < n ? sh.list[i] : 0;
+        for (int k = 2; k <= 32; k *= 2)
+            for (int j = k / 2; j > 0; j /= 2) x = exchange(x, i, k, j);
+        sh.list[i] = x;
+    }
+    for (int k = 64; k <= m; k *= 2) {
+        for (int j = k / 2; j >= 32; j /= 2) {
             __syncthreads();
             for (int p = threadIdx.x; p < m / 2; p += WARPS * 32) {
                 const int i = 2 * p - (p & (j - 1)), q = i + j;
@@ -220,6 +271,14 @@ __device__ __noinline__ void sort_list(Shared<WARPS> &sh, int n)
                 }
             }
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < m; i += WARPS * 32) {
+            u64 x = sh.list[i];
+#pragma unroll
+            for (int j = 16; j > 0; j /= 2) x = exchange(x, i, k, j);
+            sh.list[i] = x;
+        }
+    }
     __syncthreads();
 }
 
@@ -233,9 +292,9 @@ __device__ __forceinline__ float coarse_edge(int bin)
     return bin == 0 ? 0.f : __uint_as_float((uint32_t)((127 - 3) * 4 + bin - 1) << 21);
 }
 
-// The lanes' bins summed into sh.total.
+// The lanes' bins, over the row's blocks, summed into sh.total.
 template <int WARPS>
-__device__ void sum_bins(Shared<WARPS> &sh)
+__device__ void sum_bins(Shared<WARPS> &sh, int splits, int rank, int use)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __syncthreads();
@@ -248,6 +307,15 @@ __device__ void sum_bins(Shared<WARPS> &sh)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (lane == 0) sh.total[b] = d;
+    }
+    __syncthreads();
+    if (splits == 1) return;
+    if (warp < splits) st_peer(&sh.totals[use][rank][lane], warp, sh.total[lane]);
+    tc::cluster_sync();
+    if (warp == 0) {
+        u64 d = 0;
+        for (int i = 0; i < splits; ++i) d += sh.totals[use][i][lane];
+        sh.total[lane] = d;
     }
     __syncthreads();
 }
@@ -418,25 +486,32 @@ __device__ __noinline__ void bisect(Shared<WARPS> &sh, const E *z, int V, const 
 }
 
 template <typename E, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
+__global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, int splits)
 {
     constexpr int THREADS = WARPS * 32;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(raw);
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x / splits;
+    const int rank = (int)(blockIdx.x % splits);  // of the row's blocks; block 0 ends the work alone
     const E *z = reinterpret_cast<const E *>(p.logits) + row * p.ld;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int V = (int)p.V;
-    const int seg = (V + WARPS - 1) / WARPS, lo = min(V, warp * seg), hi = min(V, lo + seg);   // this warp's run
+    int runs_of_row = splits * WARPS, seg = (V + runs_of_row - 1) / runs_of_row;
+    int lo = min(V, (rank * WARPS + warp) * seg), hi = min(V, lo + seg);                        // this warp's run
+    if (tid == 0) sh.n = 0;
+    // a block's shared memory is written by others only once it runs: arrive here, wait below
+    if (splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
     tc::griddep_wait();                      // for the previous launch, before the first access
     tc::griddep_launch_dependents();
     // the thread's and the row's largest value (fmaxf passes over NaN)
     float top = -INFINITY;
     each(z, lo, hi, lane, 32, [&](int, float x) { top = fmaxf(top, x); });
-    const uint32_t kmax = (uint32_t)block_max(ordered(top), sh);
+    __syncwarp();
+    if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t kmax = (uint32_t)row_max(ordered(top), sh, splits, rank, 0);
     if (kmax <= KEY_NEG_INF) {                    // no token can be drawn
-        if (tid == 0) {
+        if (rank == 0 && tid == 0) {
             p.token[row] = -1;
             p.logprob[row] = -INFINITY;
         }
@@ -475,9 +550,39 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
         return key > thr || (key == thr && i < cut) ? (key == kmax || w >= mp ? w : 0.f) : 0.f;
     };
     bool slow = false;
-    float runs = 0.f;                             // kept weight of this warp's run, lane by lane,
-    u64 extra = 0;                                // and what else belongs to the run
+    float runs = 0.f;                             // kept weight of this warp's run, lane by lane
     bool have_runs = false;
+    float rest = 0.f;                             // sum of e^(z - max) beyond the first maximum's 1
+    // What the blocks found goes to block 0: the runs' weights, the list, a candidate.  The
+    // others are then done (false).
+    auto join = [&](bool listed, u64 best) {
+        u64 ws = fixed(runs);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+        const u64 mine = block_rest(part, equal, sh);            // its barriers also end the list's pass
+        if (lane == 0) st_peer(&sh.runs[rank * WARPS + warp], 0, ws);
+        if (tid == 0) {
+            st_peer(&sh.rests[rank], 0, mine);
+            st_peer(&sh.best[rank], 0, best);
+        }
+        if (listed && rank > 0) {
+            const int n = sh.n;
+            if (tid == 0) sh.bl = (u64)add_peer(&sh.n, 0, n);
+            __syncthreads();
+            const int at = (int)sh.bl;
+            for (int i = tid; i < n && i < CAP && at + i < CAP; i += THREADS) st_peer(&sh.list[at + i], 0, sh.list[i]);
+        }
+        if (splits > 1) tc::cluster_sync();
+        else __syncthreads();
+        if (rank > 0) return false;
+        float n = 0.f;
+        for (int i = 0; i < splits; ++i) {
+            rest += __uint_as_float((uint32_t)sh.rests[i]);
+            n += __uint_as_float((uint32_t)(sh.rests[i] >> 32));
+        }
+        rest = n - 1.f + rest;
+        return true;
+    };
 
     if (!draw) {
         int at = 0x7fffffff;
@@ -485,32 +590,35 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
             plain(gap(x));
             if (x == zmax) at = min(at, i);
         });
-        token = (int)~(uint32_t)block_max((uint32_t)~at, sh);
+        if (!join(false, block_max((uint32_t)~at, sh))) return;
+        u64 best = 0;
+        for (int i = 0; i < splits; ++i) best = max(best, sh.best[i]);
+        token = (int)~(uint32_t)best;
     } else if (by_count) {
         // a value that k of the threads' maxima reach: at least k logits do, and not many
         // more: below 1.4 k are expected while 2 k < THREADS.  Beyond, their number grows as the
-        // logarithm and soon passes CAP.
+        // logarithm and soon passes CAP.  Each block of a row finds its share of the k; the
+        // least of their values serves all.
+        const int share = (k + splits - 1) / splits;
         uint32_t floor_key = 0;
-        if (2 * k < THREADS) {
+        if (2 * share < THREADS) {
             const uint32_t own = ordered(top);
             uint32_t a = 0, b = kmax;             // count(own >= a) >= k
             while (a < b) {
                 const uint32_t mid = a + (b - a) / 2 + 1;
                 const int n = __syncthreads_count(own >= mid);
-                if (n >= k) {
+                if (n >= share) {
                     a = mid;
-                    if (n <= k + k / 8) break;
+                    if (n <= share + share / 8) break;
                 } else {
                     b = mid - 1;
                 }
             }
-            floor_key = a;
+            floor_key = ~(uint32_t)row_max((uint32_t)~a, sh, splits, rank, 1);
         } else {
             slow = true;
         }
         const float least = unordered(max(floor_key, KEY_NEG_INF));
-        if (tid == 0) sh.n = 0;
-        __syncthreads();
         each(z, lo, hi, lane, 32, [&](int i, float x) {
             plain(gap(x));
             if (x >= least && !slow) {
@@ -518,7 +626,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
                 if (at < CAP) sh.list[at] = (u64)ordered(x) << 32 | (uint32_t)~i;
             }
         });
-        __syncthreads();
+        if (!join(!slow, 0)) return;
         int n = sh.n;
         slow = slow || n > CAP;
         if (!slow) {
@@ -586,14 +694,16 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
             plain(g);
             mine[32 * coarse_bin(t)] += exp2_approx(-LOG2E * t);
         });
-        sum_bins(sh);
+        sum_bins(sh, splits, rank, 0);
         u64 sum = 0, before = 0;
 #pragma unroll
         for (int b = 0; b < BINS; ++b) sum += sh.total[b];
         const u64 target = part_of(fmaxf(tp, 0.f), sum);
         const int j = find_bin(sh, target, before);
         slow = j == BINS - 1;
-        if (!slow) {
+        if (slow) {
+            if (!join(false, 0)) return;
+        } else {
             // from here on one comparison of the logit tells where it lies: the least logits
             // whose gap falls into bin j or one before, and into one before
             const float from = coarse_edge(j), fine = BINS / (coarse_edge(j + 1) - from);
@@ -607,7 +717,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
                     mine[32 * sub(t)] += exp2_approx(-LOG2E * t);
                 }
             });
-            sum_bins(sh);
+            sum_bins(sh, splits, rank, 1);
             const int s = find_bin(sh, target, before);
             const float2 in_s = least_with(sh, kmax, [&](int w, float x) {
                 const float t = scaled(gap(x));
@@ -615,8 +725,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
             });
             in_lo = fmaxf(in_lo, in_s.x);
             in_hi = fminf(in_hi, in_s.y);         // a NaN gives way to the other
-            if (tid == 0) sh.n = 0;
-            __syncthreads();
             // what lies above the interval is kept: its weight, run by run, in the same pass
             each(z, lo, hi, lane, 32, [&](int i, float x) {
                 if (!(x >= in_lo)) return;
@@ -628,7 +736,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
                     if (at < CAP) sh.list[at] = (u64)ordered(x) << 32 | (uint32_t)~i;
                 }
             });
-            __syncthreads();
+            if (!join(true, 0)) return;
             int n = sh.n;
             slow = n > CAP;
             if (!slow) {
@@ -656,16 +764,12 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
                 thr = (uint32_t)(end >> 32);
                 cut = (int)~(uint32_t)end + (n > 0);
                 // the kept ones of the list join the runs they lie in
-                if (tid < WARPS) sh.l[tid] = 0;
-                __syncthreads();
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
                     const int i = tid * PER + e;
                     if (i < n && ((uint32_t)(sh.list[i] >> 32) == kmax || w[e] >= mp))
-                        atomicAdd(&sh.l[(int)~(uint32_t)sh.list[i] / seg], fixed(w[e]));
+                        atomicAdd(&sh.runs[(int)~(uint32_t)sh.list[i] / seg], fixed(w[e]));
                 }
-                __syncthreads();
-                extra = sh.l[warp];
                 have_runs = true;
             }
         }
@@ -675,40 +779,54 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
             plain(g);
             runs += x == zmax || w >= mp ? w : 0.f;              // no threshold but min_p
         });
+        if (!join(false, 0)) return;
         have_runs = true;
     }
-    const float rest = block_rest(part, equal, sh);               // beyond the first maximum's 1
 
     if (slow) bisect<E, WARPS>(sh, z, V, sc, kmax, by_count, k, tp, thr, cut);
     if (token < 0) {
         // the draw over the row: the sums of the runs say which one holds the answer, and
         // the block goes through that one thread by thread
         if (!have_runs) {
+            runs_of_row = WARPS, seg = (V + WARPS - 1) / WARPS;  // block 0 has the row to itself
+            lo = min(V, warp * seg), hi = min(V, lo + seg);
             runs = 0.f;
             each(z, lo, hi, lane, 32, [&](int i, float x) { runs += kept(i, x, gap(x)); });
-        }
-        u64 ws = fixed(runs);
+            u64 ws = fixed(runs);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
-        __syncthreads();
-        if (lane == 0) sh.l[warp] = ws + extra;
-        __syncthreads();
-        u64 total = 0;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) total += sh.l[w];
-        const u64 target = part_of(p.u[row], total);
-        int at = 0;                               // the run: the last with a weight if rounding leaves none
-        u64 before = 0, sum = 0;
-        for (int w = 0; w < WARPS; ++w) {
-            const u64 x = sh.l[w];
-            if (x > 0) {
-                at = w;
-                before = sum;
-                if (sum + x > target) break;
-            }
-            sum += x;
+            for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+            if (lane == 0) sh.runs[warp] = ws;
         }
-        const int first = at * seg, end = min(V, first + seg), per = (end - first + THREADS - 1) / THREADS;
+        __syncthreads();
+        // each warp by itself, some neighbouring runs a lane
+        constexpr int PER_LANE = MAX_SPLITS * WARPS / 32;
+        u64 x[PER_LANE], inc = 0, before = 0, low = 0;
+#pragma unroll
+        for (int e = 0; e < PER_LANE; ++e) {
+            const int i = lane * PER_LANE + e;
+            x[e] = i < runs_of_row ? sh.runs[i] : 0;
+            inc -= x[e];
+        }
+        low = inc, inc = 0 - inc;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const u64 target = part_of(p.u[row], __shfl_sync(0xffffffffu, inc, 31));
+        low += inc;                               // the sum of the lanes below
+        int at = -1;                              // the run: the last with a weight if rounding leaves none
+        bool found = false;
+#pragma unroll
+        for (int e = 0; e < PER_LANE; ++e) {
+            if (x[e] > 0 && !found) at = lane * PER_LANE + e, before = low, found = low + x[e] > target;
+            low += x[e];
+        }
+        const uint32_t hits = __ballot_sync(0xffffffffu, found), some = __ballot_sync(0xffffffffu, at >= 0);
+        const int from_lane = hits ? __ffs((int)hits) - 1 : some ? 31 - __clz((int)some) : 0;
+        at = max(__shfl_sync(0xffffffffu, at, from_lane), 0);
+        before = __shfl_sync(0xffffffffu, before, from_lane);
+        const int first = min(V, at * seg), end = min(V, first + seg), per = (end - first + THREADS - 1) / THREADS;
         const int from = min(end, first + tid * per), to = min(end, from + per);
         u64 own = 0, dummy;
         for (int i = from; i < to; ++i) {
@@ -735,14 +853,30 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p)
     }
 }
 
+// Blocks for a row: at least SPLIT_MIN logits each, and no more than two rounds of resident
+// blocks in all (two run on an SM, SPLIT_BLOCKS an SM are allowed).  Device time, us, with 1 / 2 /
+// 4 / 8 blocks a row: 64 rows of 32000, 36.6 / 28.7 / 26.8 / 34.6; 256 rows of 131071, two
+// blocks 114, four 118 (one, before the shorter sort, 147); one row of 32000, one block 16.1, four 14.0.
+constexpr int SPLIT_BLOCKS = 4, SPLIT_MIN = 4096;
+
 template <typename E, int WARPS>
 caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
 {
     auto kern = sample_kernel<E, WARPS>;
     constexpr size_t smem = sizeof(Shared<WARPS>);
     if (prepare_kernel_smem((const void *)kern, (int)smem) != CAAT_OK) return CAAT_ERR_CUDA;
-    launch_dependent(kern, dim3((unsigned)B), dim3(WARPS * 32), smem, s, p);
-    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    int splits = 1;
+    while (splits < MAX_SPLITS && 2 * splits * B <= SPLIT_BLOCKS * (int64_t)num_sms() && p.V >= 2 * splits * SPLIT_MIN) splits *= 2;
+    if (B * splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)(B * splits));
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = serve_attrs(attr, splits);
+    if (cudaLaunchKernelEx(&cfg, kern, p, splits) != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("sample_tokens");
     return CAAT_OK;
 }

@@ -388,6 +388,42 @@ def test_sample_extreme_rows():
     assert tok[0] == tok[1] == -1 and lp[0] == -math.inf and tok[2] == 700 and tok[3] == 600
 
 
+@pytest.mark.parametrize("V", [8193, 16400, 33001])
+@pytest.mark.parametrize("shape", ["flat", "ties", "steps", "peak"])
+def test_sample_rows_over_several_blocks(V, shape):
+    # long rows of a small batch: two, four and eight blocks a row, the last one's share short
+    B = 6
+    z = {"flat": torch.full((B, V), -1.25), "ties": torch.randint(-2, 3, (B, V), generator=_gen(8)).float(),
+         "steps": torch.arange(V).float().expand(B, V) % 10 * 0.1,
+         "peak": torch.randn(B, V, generator=_gen(9)) + 30 * (torch.arange(V) == V - 1)}[shape].clone()
+    u = np.array([0, 0.2, 0.4, 0.5, 0.75, 0.999], np.float32)
+    for top_k, top_p, min_p in ((0, 1.0, 0.0), (1, 1.0, 0.0), (0, 0.9, 0.0), (50, 0.3, 0.0), (700, 1.0, 0.0), (0, 1.0, 0.5),
+                                (3000, 0.99, 1e-4)):
+        _check_samples(z, u, 0.8, top_k, top_p, min_p)
+    _check_samples(z, u, 0.0, 0, 1.0, 0.0)
+
+
+def test_sample_extreme_rows_over_several_blocks():
+    V = 40001
+    low = torch.finfo(torch.float32).min
+    z = torch.randn(8, V, generator=_gen(11))
+    z[0] = -math.inf
+    z[1] = math.nan
+    z[2] = -math.inf
+    z[2, V - 1] = -3.0                                # one token left, in the last block's share
+    z[3, 5] = z[3, V - 7] = math.inf                  # the infinite ones share the draw
+    z[4, : V - 2] = low
+    z[5, :20000] = math.nan
+    z[6, 100:] = -math.inf                            # whole blocks without a token
+    for temp in (0.0, 0.7, 1e30):
+        for top_k, top_p in ((0, 1.0), (40, 0.9), (0, 0.6)):
+            if temp > 1 and top_p < 1:
+                continue                              # 40001 equal weights but for rounding: no one answer
+            _check_samples(z, 0.3, temp, top_k, top_p, 0.0)
+    tok, lp = _sample(z, 0.9, 1.0, 0, 1.0, 0.0)
+    assert tok[0] == tok[1] == -1 and lp[0] == -math.inf and tok[2] == V - 1 and tok[3] == V - 7
+
+
 def test_sample_rows_with_a_stride_and_odd_alignment():
     big = torch.randn(6, 5000, generator=_gen(3)).cuda()
     for dt in (torch.float32, torch.bfloat16):
