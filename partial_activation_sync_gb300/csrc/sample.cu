@@ -13,8 +13,9 @@
 // Every filter keeps a prefix of the order, so together they are one threshold: the
 // last token kept.  The row is never sorted; what is sorted, in shared memory, is a few
 // hundred candidates.
-//  - top-k: the k-th largest of the threads' own maxima bounds the k-th largest logit
-//    from below, and little more than k logits lie above it;
+//  - top-k: the k-th largest of the threads' own maxima (up to four each) bounds the k-th
+//    largest logit from below, and little more than k logits lie above it (256 rows of 131071,
+//    k = 600: 102 us, by the bisection below 2756);
 //  - top-p alone: two histogram passes find the narrow interval in which the prefix ends:
 //    32 bins over the gap to the largest logit, four to an octave, then 32 equal parts of
 //    the bin where the weight is reached.  Each lane has its own bins (a column of shared
@@ -505,8 +506,13 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, i
     tc::griddep_wait();                      // for the previous launch, before the first access
     tc::griddep_launch_dependents();
     // the thread's and the row's largest value (fmaxf passes over NaN)
-    float top = -INFINITY;
-    each(z, lo, hi, lane, 32, [&](int, float x) { top = fmaxf(top, x); });
+    // the thread's as four, which take its values in turn
+    float four[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    each(z, lo, hi, lane, 32, [&](int, float x) {
+        const float m = fmaxf(four[0], x);
+        four[0] = four[1], four[1] = four[2], four[2] = four[3], four[3] = m;
+    });
+    const float top = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
     __syncwarp();
     if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     const uint32_t kmax = (uint32_t)row_max(ordered(top), sh, splits, rank, 0);
@@ -595,18 +601,28 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, i
         for (int i = 0; i < splits; ++i) best = max(best, sh.best[i]);
         token = (int)~(uint32_t)best;
     } else if (by_count) {
-        // a value that k of the threads' maxima reach: at least k logits do, and not many
-        // more: below 1.4 k are expected while 2 k < THREADS.  Beyond, their number grows as the
-        // logarithm and soon passes CAP.  Each block of a row finds its share of the k; the
+        // A value that k of the threads' maxima reach: at least k logits do, and not many
+        // more: below 1.4 k are expected while 2 k is below the number of maxima.  Beyond, theirs
+        // grows as the logarithm and soon passes CAP.  One maximum a thread, which costs a
+        // barrier a step, or all four.  Each block of a row finds its share of the k; the
         // least of their values serves all.
         const int share = (k + splits - 1) / splits;
+        const bool one = 2 * share < THREADS;
+        slow = 2 * share >= 4 * THREADS;
         uint32_t floor_key = 0;
-        if (2 * share < THREADS) {
-            const uint32_t own = ordered(top);
-            uint32_t a = 0, b = kmax;             // count(own >= a) >= k
+        if (!slow) {
+            uint32_t a = 0, b = kmax;             // count(maxima >= a) >= share
             while (a < b) {
                 const uint32_t mid = a + (b - a) / 2 + 1;
-                const int n = __syncthreads_count(own >= mid);
+                int n;
+                if (one) {
+                    n = __syncthreads_count(ordered(top) >= mid);
+                } else {
+                    n = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) n += ordered(four[e]) >= mid;
+                    n = (int)block_sum((u64)n, sh);
+                }
                 if (n >= share) {
                     a = mid;
                     if (n <= share + share / 8) break;
@@ -615,8 +631,6 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, i
                 }
             }
             floor_key = ~(uint32_t)row_max((uint32_t)~a, sh, splits, rank, 1);
-        } else {
-            slow = true;
         }
         const float least = unordered(max(floor_key, KEY_NEG_INF));
         each(z, lo, hi, lane, 32, [&](int i, float x) {
