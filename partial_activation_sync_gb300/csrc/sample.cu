@@ -31,8 +31,8 @@
 // sums over distributed shared memory; then the first takes the others' candidates and
 // runs' weights and ends the work alone.  The passes after the first find the row in L2 or
 // L1.  Bound by the instructions of those passes for large batches and by the latency of the
-// chain for few rows (device time): 14.0 us for one row of 32000 (bf16), 26.8 us for 64 of
-// them (fp32), 114 us for 256 rows of 131071 (bf16).
+// chain for few rows (device time): 14.4 us for one row of 32000 (bf16), 26.8 us for 64 of
+// them (fp32), 92 us for 256 rows of 131071 (bf16).
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -486,15 +486,50 @@ __device__ __noinline__ void bisect(Shared<WARPS> &sh, const E *z, int V, const 
     cut_out = cut;
 }
 
+constexpr int MAX_ORDERED = 1024;               // rows that costly_first takes
+
+// The n-th of `rows` rows, those with top-p alone first: their histograms take several times
+// the others' passes, and one that starts last keeps the others waiting.  For all threads;
+// words: one for 32 rows, not used before the next barrier.
+__device__ __noinline__ int costly_first(const float *temperature, const int32_t *top_k, const float *top_p, int64_t V, int rows,
+                                         int n, uint32_t *words)
+{
+    const int all = (rows + 31) / 32, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < 32 * all; i += blockDim.x) {
+        const int j = min(i, rows - 1), k = top_k[j];
+        const float T = temperature[j], tp = top_p[j];       // loaded together, not one after the other
+        const uint32_t m = __ballot_sync(0xffffffffu, (i < rows) & (T > 0.f) & (tp < 1.f) & ((k <= 0) | (k >= V)));
+        if (lane == 0) words[i >> 5] = m;
+    }
+    __syncthreads();
+    // lane w: the word w, and how many costly rows lie before and in all
+    const uint32_t m = lane < all ? words[lane] : 0u;
+    int inc = __popc(m);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    const int costly = __shfl_sync(0xffffffffu, inc, 31);
+    // the word that holds the one sought, then its place in the word
+    const bool first = n < costly;
+    const int in_word = first ? __popc(m) : max(min(32, rows - 32 * lane), 0) - __popc(m);
+    const int before = (first ? inc : min(32 * lane + 32, rows) - inc) - in_word, sought = first ? n : n - costly;
+    const int w = __ffs((int)__ballot_sync(0xffffffffu, before <= sought && sought < before + in_word)) - 1;
+    const int place = sought - __shfl_sync(0xffffffffu, before, w);
+    const uint32_t bits = first ? __shfl_sync(0xffffffffu, m, w) : ~__shfl_sync(0xffffffffu, m, w);
+    const bool mine = (bits >> lane & 1u) != 0 && __popc(bits & ((1u << lane) - 1)) == place;
+    return 32 * w + __ffs((int)__ballot_sync(0xffffffffu, mine)) - 1;
+}
+
 template <typename E, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, int splits)
+__global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, int splits, int ordered_rows)
 {
     constexpr int THREADS = WARPS * 32;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared<WARPS> &sh = *reinterpret_cast<Shared<WARPS> *>(raw);
-    const int64_t row = blockIdx.x / splits;
+    int64_t row = blockIdx.x / splits;
     const int rank = (int)(blockIdx.x % splits);  // of the row's blocks; block 0 ends the work alone
-    const E *z = reinterpret_cast<const E *>(p.logits) + row * p.ld;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int V = (int)p.V;
     int runs_of_row = splits * WARPS, seg = (V + runs_of_row - 1) / runs_of_row;
@@ -505,6 +540,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, i
 
     tc::griddep_wait();                      // for the previous launch, before the first access
     tc::griddep_launch_dependents();
+    if (ordered_rows > 0) row = costly_first(p.temperature, p.top_k, p.top_p, p.V, ordered_rows, (int)row,
+                                              reinterpret_cast<uint32_t *>(sh.total));
+    const E *z = reinterpret_cast<const E *>(p.logits) + row * p.ld;
     // the thread's and the row's largest value (fmaxf passes over NaN)
     // the thread's as four, which take its values in turn
     float four[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -870,7 +908,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) sample_kernel(SampleParams p, i
 // Blocks for a row: at least SPLIT_MIN logits each, and no more than two rounds of resident
 // blocks in all (two run on an SM, SPLIT_BLOCKS an SM are allowed).  Device time, us, with 1 / 2 /
 // 4 / 8 blocks a row: 64 rows of 32000, 36.6 / 28.7 / 26.8 / 34.6; 256 rows of 131071, two
-// blocks 114, four 118 (one, before the shorter sort, 147); one row of 32000, one block 16.1, four 14.0.
+// blocks 115, four 118 (one, before the shorter sort, 147); one row of 32000, one block 16.1, four 14.0.
 constexpr int SPLIT_BLOCKS = 4, SPLIT_MIN = 4096;
 
 template <typename E, int WARPS>
@@ -882,6 +920,9 @@ caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
     int splits = 1;
     while (splits < MAX_SPLITS && 2 * splits * B <= SPLIT_BLOCKS * (int64_t)num_sms() && p.V >= 2 * splits * SPLIT_MIN) splits *= 2;
     if (B * splits > 0x7fffffff) return CAAT_ERR_INVALID_ARG;
+    // More blocks than are resident (two an SM): the costly rows first (256 rows of 131071 of every
+    // kind 92 us, in the batch's order 115; rows of one kind 61 against 59).
+    const int ordered_rows = B * splits > 2 * (int64_t)num_sms() && B <= MAX_ORDERED ? (int)B : 0;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)(B * splits));
@@ -890,7 +931,7 @@ caat_status launch(int64_t B, const SampleParams &p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = serve_attrs(attr, splits);
-    if (cudaLaunchKernelEx(&cfg, kern, p, splits) != cudaSuccess) return CAAT_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, p, splits, ordered_rows) != cudaSuccess) return CAAT_ERR_CUDA;
     note_launch("sample_tokens");
     return CAAT_OK;
 }

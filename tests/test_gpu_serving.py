@@ -403,6 +403,18 @@ def test_sample_rows_over_several_blocks(V, shape):
     _check_samples(z, u, 0.0, 0, 1.0, 0.0)
 
 
+@pytest.mark.parametrize("B,V,kind", [(305, 700, "mixed"), (417, 700, "mixed"), (320, 700, "costly"), (309, 700, "cheap"),
+                                      (1025, 90, "mixed"), (161, 9001, "mixed")])
+def test_sample_more_rows_than_run_at_once(B, V, kind):
+    # rows with top-p alone start first, wherever they stand in the batch
+    g = _gen(B)
+    z = torch.randn(B, V, generator=g) * 2
+    r = np.arange(B)
+    p = {"mixed": np.where(r % 3 == 0, 0.8, 1.0), "costly": 0.7, "cheap": 1.0}[kind]
+    k = {"mixed": np.where(r % 5 == 1, 20, 0), "costly": 0, "cheap": np.where(r % 2 == 0, 9, 0)}[kind]
+    _check_samples(z, torch.rand(B, generator=g).numpy(), np.where(r % 7 == 6, 0.0, 0.9), k, p, 0.0)
+
+
 def test_sample_extreme_rows_over_several_blocks():
     V = 40001
     low = torch.finfo(torch.float32).min
