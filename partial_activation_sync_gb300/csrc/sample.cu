@@ -488,8 +488,8 @@ __device__ __noinline__ void bisect(Shared<WARPS> &sh, const E *z, int V, const 
 
 constexpr int MAX_ORDERED = 1024;               // rows that costly_first takes
 
-// The n-th of `rows` rows, those with top-p alone first: their histograms take several times
-// the others' passes, and one that starts last keeps the others waiting.  For all threads;
+// The n-th of `rows` rows, those with top-p alone first: their histograms take two to
+// three times the others' passes, and one that starts last keeps the others waiting.  For all threads;
 // words: one for 32 rows, not used before the next barrier.
 __device__ __noinline__ int costly_first(const float *temperature, const int32_t *top_k, const float *top_p, int64_t V, int rows,
                                          int n, uint32_t *words)
